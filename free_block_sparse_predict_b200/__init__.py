@@ -19,6 +19,8 @@ import torch
 
 from ._native import (SPARGE_BF16, SPARGE_F16, SPARGE_F32, SpargeError, SpargeParams,
                       SpargeStats, lib, lib_path)
+from .serving import (Rope, grid_positions, rope_frequencies, sparge_rope_apply,
+                      sparge_rope_inverse)
 
 __all__ = [
     "SpargeError", "SpargeParams", "SpargeStats", "make_params", "lib_path",
@@ -27,6 +29,7 @@ __all__ = [
     "sparge_predict_pool", "sparge_predict_select", "sparge_predict_mask_noalloc",
     "sparge_mask_compact", "sparge_attn_fwd", "sparge_device_status",
     "sparge_selftest_wait_timeout", "sparge_status_string",
+    "Rope", "rope_frequencies", "grid_positions", "sparge_rope_apply", "sparge_rope_inverse",
     "workspace", "predict_outputs", "sparge_forward",
 ]
 
@@ -242,18 +245,28 @@ def predict_outputs(params: SpargeParams, device="cuda"):
             torch.empty((B, Hkv, Tn), dtype=torch.float32, device=device))
 
 
-def sparge_forward(params, q, k, v, perm=None, ws=None, stats=None, stream=None):
-    """permute (optional) -> predict -> attention -> inverse permute.
+def sparge_forward(params, q, k, v, perm=None, ws=None, stats=None, stream=None, rope=None):
+    """rotary positions and permute (optional) -> predict -> attention -> inverse permute.
 
     Returns (o, mask, kv_idx, kv_cnt).  ``perm`` is a device table from
-    sparge_hilbert_index; ``ws`` a workspace of sparge_workspace_bytes."""
+    sparge_hilbert_index; ``ws`` a workspace of sparge_workspace_bytes; ``rope`` a
+    Rope whose angles turn q and k first, in the same pass that permutes them (q and
+    k may then have any strides)."""
     dev = q.device
     if ws is None:
         ws = workspace(params, dev)
+    if rope is not None:
+        qp, kp = (torch.empty(x.shape, dtype=x.dtype, device=dev) for x in (q, k))
+        for x, y in ((q, qp), (k, kp)):
+            sparge_rope_apply(x, y, rope.pos, rope.inv_freq, rope.axis, perm, rope.interleaved,
+                              stream)
+        q, k = qp, kp
     if perm is not None:
-        qp, kp, vp = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        sparge_hilbert_permute(q, qp, perm, stream)
-        sparge_hilbert_permute(k, kp, perm, stream)
+        if rope is None:
+            qp, kp = torch.empty_like(q), torch.empty_like(k)
+            sparge_hilbert_permute(q, qp, perm, stream)
+            sparge_hilbert_permute(k, kp, perm, stream)
+        vp = torch.empty_like(v)
         sparge_hilbert_permute(v, vp, perm, stream)
         q, k, v = qp, kp, vp
     mask, kv_idx, kv_cnt, s_q, s_k = predict_outputs(params, dev)

@@ -32,7 +32,16 @@ class SpargeStats(ctypes.Structure):
                 ("skipped_slices", ctypes.c_uint64)]
 
 
+class SpargeRope(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("rot", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3),
+                ("pos_stride", ctypes.c_int64)]
+
+
 _P = ctypes.POINTER(SpargeParams)
+_R = ctypes.POINTER(SpargeRope)
 _V = ctypes.c_void_p
 _I = ctypes.c_int32
 _S = ctypes.c_size_t
@@ -49,6 +58,8 @@ SIGNATURES = {
     "sparge_predict_select": (ctypes.c_int, [_P, _V, _V, _V, _V, _V, _V, _S, _V]),
     "sparge_mask_compact": (ctypes.c_int, [_P, _V, _V, _V, _V]),
     "sparge_attn_fwd": (ctypes.c_int, [_P, _V, _V, _V, _V, _V, _V, _V, _S, _V, _V]),
+    "sparge_rope_apply": (ctypes.c_int, [_R, _V, _V, _V, _V, _V, _V, _V]),
+    "sparge_rope_inverse": (ctypes.c_int, [_R, _V, _V, _V, _V, _V, _V, _V]),
     "sparge_device_status": (ctypes.c_int, [_V, _V]),
     "sparge_selftest_wait_timeout": (ctypes.c_int, [_V, _V]),
     "sparge_status_string": (ctypes.c_char_p, [ctypes.c_int]),

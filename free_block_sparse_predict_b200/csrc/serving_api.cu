@@ -1,0 +1,125 @@
+// extern "C" entry points around the prompt pass: argument validation and
+// launches of the rotary-position, paging and 4-bit-cache kernels on the
+// caller's stream.  See include/sparge.h.
+#include <cmath>
+#include <cstdint>
+
+#include "sparge_internal.h"
+
+using namespace sparge;
+
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+sparge_status_t from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return SPARGE_OK;
+  if (e == cudaErrorNotSupported) return SPARGE_EUNSUPPORTED;
+  return SPARGE_ECUDA;
+}
+
+bool is_dtype(sparge_dtype_t t) { return t == SPARGE_F16 || t == SPARGE_BF16 || t == SPARGE_F32; }
+int64_t elem_size(sparge_dtype_t t) { return t == SPARGE_F32 ? 4 : 2; }
+
+// Rows of `row` bytes at every index of ext[n] with strides in bytes.
+struct Rows {
+  int64_t ext[3], stride[3];
+  int64_t row;
+};
+
+// Bytes from the first to one past the last; -1 when it does not fit 62 bits.
+int64_t extent(const Rows& r) {
+  int64_t sum = r.row;
+  for (int i = 0; i < 3; ++i) {
+    const int64_t n = r.ext[i] - 1;
+    if (n > 0 && r.stride[i] > (int64_t(1) << 61) / n) return -1;
+    sum += n * r.stride[i];
+    if (sum > (int64_t(1) << 61)) return -1;
+  }
+  return sum;
+}
+
+// Whether each stride, in ascending order, steps over what the smaller span.
+bool disjoint(Rows r) {
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j + 1 < 3; ++j)
+      if (r.stride[j] > r.stride[j + 1]) {
+        const int64_t s = r.stride[j], e = r.ext[j];
+        r.stride[j] = r.stride[j + 1], r.ext[j] = r.ext[j + 1];
+        r.stride[j + 1] = s, r.ext[j + 1] = e;
+      }
+  int64_t span = r.row;
+  for (int i = 0; i < 3; ++i) {
+    if (r.ext[i] <= 1) continue;
+    if (r.stride[i] < span) return false;
+    span += (r.ext[i] - 1) * r.stride[i];
+  }
+  return true;
+}
+
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + uintptr_t(nb) && y < x + uintptr_t(na);
+}
+
+}  // namespace
+
+extern "C" {
+
+static sparge_status_t rope_common(const sparge_rope_t* p, const void* src, void* dst,
+                                   const int32_t* pos, const double* inv_freq,
+                                   const int32_t* axis, const int32_t* perm, bool inverse,
+                                   cudaStream_t stream) {
+  if (p == nullptr) return SPARGE_EINVAL;
+  if (p->B < 0 || p->H < 0 || p->N < 0 || p->d < 1 || p->axes < 1) return SPARGE_EINVAL;
+  if (p->rot < 2 || p->rot > p->d || p->rot % 2 != 0) return SPARGE_EINVAL;
+  if ((p->interleaved != 0 && p->interleaved != 1) || !is_dtype(p->dtype)) return SPARGE_EINVAL;
+  if (p->pos_stride < 0 || p->pos_stride > (int64_t(1) << 40)) return SPARGE_EINVAL;
+  const int64_t es = elem_size(p->dtype);
+  if (p->d * es % 16 != 0 || p->rot * es % 32 != 0) return SPARGE_EUNSUPPORTED;
+  Rows r[2];
+  for (int i = 0; i < 2; ++i) {
+    const int64_t* st = (i == 0) != inverse ? p->x_stride : p->y_stride;  // r[0]: the source
+    r[i] = Rows{{p->B, p->H, p->N}, {0, 0, 0}, p->d * es};
+    for (int k = 0; k < 3; ++k) {
+      if (r[i].ext[k] <= 1) continue;
+      if (st[k] < 0 || st[k] > (int64_t(1) << 58)) return SPARGE_EINVAL;
+      r[i].stride[k] = st[k] * es;
+      if (r[i].stride[k] % 16 != 0) return SPARGE_EUNSUPPORTED;
+    }
+  }
+  if (p->B == 0 || p->H == 0 || p->N == 0) return SPARGE_OK;
+  if (int64_t(p->B) * p->H > INT32_MAX) return SPARGE_EUNSUPPORTED;
+  if (src == nullptr || dst == nullptr || pos == nullptr || inv_freq == nullptr || axis == nullptr)
+    return SPARGE_EINVAL;
+  if (!aligned(src, 16) || !aligned(dst, 16) || !aligned(pos, 4) || !aligned(inv_freq, 8) ||
+      !aligned(axis, 4) || !aligned(perm, 4))
+    return SPARGE_EINVAL;
+  const int64_t ns = extent(r[0]), nd = extent(r[1]);
+  if (ns < 0 || nd < 0 || !disjoint(r[1])) return SPARGE_EINVAL;
+  bool same = src == dst && perm == nullptr;
+  for (int k = 0; k < 3; ++k) same = same && r[0].stride[k] == r[1].stride[k];
+  if (!same && overlap(src, ns, dst, nd)) return SPARGE_EINVAL;
+  DeviceScope dev;
+  const sparge_status_t st = dev.enter(dst);
+  if (st != SPARGE_OK) return st;
+  int64_t ss[3], ds[3];
+  for (int k = 0; k < 3; ++k) ss[k] = r[0].stride[k], ds[k] = r[1].stride[k];
+  return from_cuda(
+      launch_rope(*p, src, ss, dst, ds, pos, inv_freq, axis, perm, inverse, stream));
+}
+
+sparge_status_t sparge_rope_apply(const sparge_rope_t* p, const void* x, void* y,
+                                  const int32_t* pos, const double* inv_freq,
+                                  const int32_t* axis, const int32_t* perm, cudaStream_t stream) {
+  return rope_common(p, x, y, pos, inv_freq, axis, perm, false, stream);
+}
+
+sparge_status_t sparge_rope_inverse(const sparge_rope_t* p, const void* y, void* x,
+                                    const int32_t* pos, const double* inv_freq,
+                                    const int32_t* axis, const int32_t* perm,
+                                    cudaStream_t stream) {
+  return rope_common(p, y, x, pos, inv_freq, axis, perm, true, stream);
+}
+
+}  // extern "C"

@@ -138,6 +138,13 @@ cudaError_t launch_hilbert_index(int32_t N, int32_t prefix_len, int32_t T, int32
 cudaError_t launch_permute_rows(const void* x, void* y, int64_t BH, int32_t N, int32_t row_bytes,
                                 const int32_t* perm, bool inverse, cudaStream_t s);
 
+// ------------------------------------------------------------- rope.cu
+// strides in bytes, batches / heads / tokens
+cudaError_t launch_rope(const sparge_rope_t& p, const void* src, const int64_t* src_stride,
+                        void* dst, const int64_t* dst_stride, const int32_t* pos,
+                        const double* inv_freq, const int32_t* axis, const int32_t* perm,
+                        bool inverse, cudaStream_t s);
+
 // ------------------------------------------------------------- attn_sm100.cu
 struct AttnPtrs {
   const void* q;        // io dtype, or int8 codes with qk_int8

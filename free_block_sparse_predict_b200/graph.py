@@ -17,7 +17,8 @@ import torch
 
 from . import (SPARGE_BF16, SPARGE_F16, SPARGE_F32, predict_outputs, sparge_attn_fwd,
                sparge_hilbert_index, sparge_hilbert_permute, sparge_hilbert_workspace_bytes,
-               sparge_inverse_permute, sparge_predict_pool, sparge_predict_select, workspace)
+               sparge_inverse_permute, sparge_predict_pool, sparge_predict_select,
+               sparge_rope_apply, workspace)
 
 _TD = {SPARGE_F16: torch.float16, SPARGE_BF16: torch.bfloat16, SPARGE_F32: torch.float32}
 
@@ -27,13 +28,15 @@ class SpargeGraph:
 
     params: SpargeParams of the problem.  grid: optional (prefix_len, T, Hg, Wg)
     of a token grid; with it the graph builds the Hilbert table, permutes Q, K,
-    V, and puts O back in token order, all inside the graph."""
+    V, and puts O back in token order, all inside the graph.  rope: optional Rope
+    (kept by the graph, which reads its positions at every replay): Q and K are
+    turned in the pass that permutes them."""
 
-    def __init__(self, params, grid=None, device="cuda"):
+    def __init__(self, params, grid=None, device="cuda", rope=None):
         dev = torch.device(device)
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        self.params, self.grid, self.device = params, grid, dev
+        self.params, self.grid, self.device, self.rope = params, grid, dev, rope
         p = params
         io, od = _TD[p.io_dtype], _TD[p.o_dtype]
         self.q = torch.zeros((p.B, p.Hq, p.N, p.d), dtype=io, device=dev)
@@ -47,8 +50,9 @@ class SpargeGraph:
             self.perm = torch.empty(p.N, dtype=torch.int32, device=dev)
             self.hws = torch.zeros(sparge_hilbert_workspace_bytes(T, Hg, Wg),
                                    dtype=torch.uint8, device=dev)
-            self.qp, self.kp, self.vp = (torch.empty_like(x) for x in (self.q, self.k, self.v))
-            self.op = torch.empty_like(self.o)
+            self.vp, self.op = torch.empty_like(self.v), torch.empty_like(self.o)
+        if grid is not None or rope is not None:
+            self.qp, self.kp = torch.empty_like(self.q), torch.empty_like(self.k)
         self.graph = torch.cuda.CUDAGraph()
         side = torch.cuda.Stream(dev)
         side.wait_stream(torch.cuda.current_stream(dev))
@@ -63,13 +67,22 @@ class SpargeGraph:
     def _forward(self):
         p = self.params
         q, k, v, o = self.q, self.k, self.v, self.o
+        perm = None
         if self.grid is not None:
             prefix, T, Hg, Wg = self.grid
-            sparge_hilbert_index(p.N, prefix, T, Hg, Wg, self.perm, self.hws)
-            sparge_hilbert_permute(q, self.qp, self.perm)
-            sparge_hilbert_permute(k, self.kp, self.perm)
-            sparge_hilbert_permute(v, self.vp, self.perm)
-            q, k, v, o = self.qp, self.kp, self.vp, self.op
+            perm = self.perm
+            sparge_hilbert_index(p.N, prefix, T, Hg, Wg, perm, self.hws)
+            if self.rope is None:
+                sparge_hilbert_permute(q, self.qp, perm)
+                sparge_hilbert_permute(k, self.kp, perm)
+            sparge_hilbert_permute(v, self.vp, perm)
+            v, o = self.vp, self.op
+        if self.rope is not None:
+            r = self.rope
+            sparge_rope_apply(q, self.qp, r.pos, r.inv_freq, r.axis, perm, r.interleaved)
+            sparge_rope_apply(k, self.kp, r.pos, r.inv_freq, r.axis, perm, r.interleaved)
+        if perm is not None or self.rope is not None:
+            q, k = self.qp, self.kp
         sparge_predict_pool(p, q, k, self.ws)
         sparge_predict_select(p, self.mask, self.kv_idx, self.kv_cnt, None, None, self.ws)
         sparge_attn_fwd(p, q, k, v, self.kv_idx, self.kv_cnt, o, self.ws)

@@ -1,0 +1,142 @@
+"""Binding of the entry points around the prompt pass (include/sparge.h): rotary
+positions with several axes.
+
+As in the package's main module, every ``sparge_*`` function has the name of the
+C entry point it wraps and only checks and marshals arguments; a call runs on the
+device that owns its tensors, on that device's current stream unless one is given.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+from ._native import (SPARGE_BF16, SPARGE_F16, SPARGE_F32, SpargeError, SpargeRope, lib)
+
+__all__ = ["Rope", "rope_frequencies", "grid_positions", "sparge_rope_apply",
+           "sparge_rope_inverse"]
+
+_DT = {torch.float16: SPARGE_F16, torch.bfloat16: SPARGE_BF16, torch.float32: SPARGE_F32}
+
+
+def _bad(msg: str) -> SpargeError:
+    return SpargeError(1, msg)
+
+
+def _check(code: int) -> None:
+    if code != 0:
+        raise SpargeError(code, lib().sparge_status_string(code).decode())
+
+
+def _stream(stream, device) -> int:
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _device(t: torch.Tensor, name: str):
+    if not t.is_cuda:
+        raise _bad(f"{name}: expected a CUDA tensor")
+    return t.device
+
+
+def _flat(t, name: str, numel: int, dtype, device) -> int:
+    """Address of a contiguous tensor of at least numel elements of dtype on device."""
+    if t.device != device:
+        raise _bad(f"{name}: expected a tensor on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise _bad(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise _bad(f"{name}: expected a contiguous tensor")
+    if t.numel() < numel:
+        raise _bad(f"{name}: needs {numel} elements, has {t.numel()}")
+    return t.data_ptr()
+
+
+# ----------------------------------------------------------------------------
+# rotary positions
+# ----------------------------------------------------------------------------
+
+class Rope(NamedTuple):
+    """Rotary positions of one token sequence, as sparge_forward and SpargeGraph take them."""
+    pos: torch.Tensor        # int32 [axes, N] or [B, axes, N]
+    inv_freq: torch.Tensor   # float64 [pairs], radians per position
+    axis: torch.Tensor       # int32 [pairs], the axis that turns each pair
+    interleaved: bool = False
+
+
+def rope_frequencies(pairs, theta: float = 1e4, joint: bool = False, device="cuda"):
+    """(inv_freq, axis) for ``pairs[a]`` channel pairs turned by axis a, in that order.
+
+    Each axis has the whole spectrum theta^(-i / pairs[a]); with ``joint`` one spectrum
+    theta^(-i / sum(pairs)) runs through all axes' pairs."""
+    total = sum(pairs)
+    if joint:
+        f = -torch.arange(total, dtype=torch.float64) / total
+    else:
+        f = torch.cat([-torch.arange(n, dtype=torch.float64) / max(n, 1) for n in pairs])
+    axis = torch.cat([torch.full((n,), a, dtype=torch.int32) for a, n in enumerate(pairs)])
+    return (theta ** f).to(device), axis.to(device)
+
+
+def grid_positions(N: int, prefix_len: int, T: int, Hg: int, Wg: int, device="cuda"):
+    """Positions [3, N] (time, height, width) of a sequence with a T x Hg x Wg token grid
+    behind prefix_len text tokens: text counts up on all axes at once, the grid's axes start
+    where the text ends, and what follows goes on from the grid's largest coordinate."""
+    L = T * Hg * Wg
+    if min(N, prefix_len) < 0 or min(T, Hg, Wg) < 1 or prefix_len + L > N:
+        raise _bad("the grid does not fit the sequence")
+    pos = torch.empty((3, N), dtype=torch.int32)
+    pos[:, :prefix_len] = torch.arange(prefix_len, dtype=torch.int32)
+    g = torch.stack(torch.meshgrid(*(torch.arange(n, dtype=torch.int32) for n in (T, Hg, Wg)),
+                                   indexing="ij"))
+    pos[:, prefix_len:prefix_len + L] = prefix_len + g.reshape(3, L)
+    rest = N - prefix_len - L
+    pos[:, N - rest:] = prefix_len + max(T, Hg, Wg) + torch.arange(rest, dtype=torch.int32)
+    return pos.to(device)
+
+
+def _rope(inverse, x, y, pos, inv_freq, axis, perm, interleaved, stream):
+    dev = _device(x, "x")
+    if x.dim() != 4 or x.shape != y.shape or x.dtype != y.dtype or x.dtype not in _DT:
+        raise _bad("expected two [B, H, N, d] tensors of one shape and floating dtype")
+    if y.device != dev:
+        raise _bad(f"y: expected a tensor on {dev}, got {y.device}")
+    B, H, N, d = x.shape
+    sx, sy = x.stride(), y.stride()
+    if d > 1 and (sx[3] != 1 or sy[3] != 1):
+        raise _bad("the channels have to be contiguous")
+    if pos.dim() not in (2, 3) or pos.shape[-1] != N or (pos.dim() == 3 and pos.shape[0] != B):
+        raise _bad("pos: expected [axes, N] or [B, axes, N]")
+    if pos.dtype != torch.int32 or pos.device != dev:
+        raise _bad(f"pos: expected {torch.int32} on {dev}")
+    axes, sp = pos.shape[-2], pos.stride()
+    if (N > 1 and sp[-1] != 1) or (axes > 1 and sp[-2] != N):
+        raise _bad("pos: expected contiguous [axes, N] rows")
+    pairs = inv_freq.numel()
+    p = SpargeRope(B, H, N, d, 2 * pairs, axes, int(interleaved), _DT[x.dtype],
+                   (sx[0], sx[1], sx[2]), (sy[0], sy[1], sy[2]), sp[0] if pos.dim() == 3 else 0)
+    args = (pos.data_ptr(), _flat(inv_freq, "inv_freq", pairs, torch.float64, dev),
+            _flat(axis, "axis", pairs, torch.int32, dev),
+            None if perm is None else _flat(perm, "perm", N, torch.int32, dev),
+            _stream(stream, dev))
+    if inverse:
+        _check(lib().sparge_rope_inverse(ctypes.byref(p), y.data_ptr(), x.data_ptr(), *args))
+    else:
+        _check(lib().sparge_rope_apply(ctypes.byref(p), x.data_ptr(), y.data_ptr(), *args))
+
+
+def sparge_rope_apply(x, y, pos, inv_freq, axis, perm: Optional[torch.Tensor] = None,
+                      interleaved: bool = False, stream=None) -> None:
+    """y[b, h, p] = x[b, h, s] turned by the angles pos[b, axis, s] * inv_freq, s = perm[p].
+
+    x, y: [B, H, N, d] of any strides (a transposed [B, N, H, d], some heads of a packed
+    projection); y may be x.  Pairs behind len(inv_freq) stay as they are."""
+    _rope(False, x, y, pos, inv_freq, axis, perm, interleaved, stream)
+
+
+def sparge_rope_inverse(y, x, pos, inv_freq, axis, perm: Optional[torch.Tensor] = None,
+                        interleaved: bool = False, stream=None) -> None:
+    """x[b, h, s] = y[b, h, p] turned back: the inverse of sparge_rope_apply and its gradient."""
+    _rope(True, x, y, pos, inv_freq, axis, perm, interleaved, stream)

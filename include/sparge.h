@@ -53,7 +53,8 @@ typedef enum {
   SPARGE_ECUDA = 3,
   SPARGE_ETIMEOUT = 4,
   SPARGE_EWORKSPACE = 5,
-  SPARGE_ERANGE = 6 /* a bf16 V value did not fit fp16 (P~V runs in fp16); it was saturated */
+  SPARGE_ERANGE = 6 /* a value did not fit its narrower form and was saturated: a bf16 V value
+                       in fp16 (P~V runs in fp16), or the scale of a 4-bit cache group */
 } sparge_status_t;
 
 typedef enum { SPARGE_F16 = 0, SPARGE_BF16 = 1, SPARGE_F32 = 2 } sparge_dtype_t;
@@ -204,6 +205,54 @@ sparge_status_t sparge_attn_fwd(const sparge_params_t* p, const void* q, const v
                                 const void* v, const int32_t* kv_idx, const int32_t* kv_cnt,
                                 void* o, void* ws, size_t ws_bytes, sparge_stats_t* stats,
                                 cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Around the prompt pass: positions, pages and the tokens that follow.
+ *
+ * The paper has no counterpart of these calls.  They are what a serving
+ * program runs next to the sparse prompt pass: rotary positions of Q and K
+ * (fused with the Hilbert permutation), the block tables and slots of a paged
+ * cache, the cache itself with K and V in 4 bits, and attention of new tokens
+ * over it.  Conventions as above, except where strides are given.
+ * ------------------------------------------------------------------------- */
+
+/* Rotary positions with several axes (time, height, width, ...). */
+typedef struct {
+  int32_t B, H, N, d;     /* x, y: [B, H, N, d], channels contiguous, the rest strided     */
+  int32_t rot;            /* channels that turn, the first rot of d; the others are copied */
+  int32_t axes;           /* position axes, >= 1                                           */
+  int32_t interleaved;    /* pair i is channels (i, i + rot/2), or with 1 (2i, 2i + 1)     */
+  sparge_dtype_t dtype;   /* of x and y                                                    */
+  int64_t x_stride[3];    /* elements between batches, heads and tokens of x, and of y;    */
+  int64_t y_stride[3];    /*   each a multiple of 16 bytes                                 */
+  int64_t pos_stride;     /* elements between the positions of two batches; 0 shares them  */
+} sparge_rope_t;
+
+/* y[b, h, p, :] = x[b, h, s, :] turned, s = perm[p] (perm == NULL: s = p): pair i, (u, v),
+ * becomes (u cos a - v sin a, u sin a + v cos a) with a = pos[b, axis[i], s] * inv_freq[i].
+ *   pos       device int32 [B or 1, axes, N]
+ *   inv_freq  device float64 [rot/2], radians per position (any frequency scaling is in it)
+ *   axis      device int32 [rot/2], which axis turns pair i, in [0, axes) (others: a = 0)
+ *   perm      device int32 [N] or NULL; rows whose entry lies outside [0, N) are skipped
+ * The angle is reduced in float64 turns, so far positions lose nothing: for |inv_freq| <= 1 its
+ * error is below 2^-23 of a turn up to position 2^30.  The products are float32, rounded once
+ * to dtype.
+ * y may be x (same strides, no perm); any other overlap of the two extents is refused
+ * (SPARGE_EINVAL), as is a written tensor whose rows may overlap: its strides, in ascending
+ * order, must each step over what the smaller ones span (no stride of 0, so no broadcast).
+ * SPARGE_EUNSUPPORTED: rows or strides that are no multiple of 16 bytes, or rot * element size
+ * no multiple of 32 bytes. */
+sparge_status_t sparge_rope_apply(const sparge_rope_t* p, const void* x, void* y,
+                                  const int32_t* pos, const double* inv_freq,
+                                  const int32_t* axis, const int32_t* perm, cudaStream_t stream);
+
+/* The inverse, which is also the gradient of sparge_rope_apply (the rotation is
+ * orthogonal): x[b, h, s, :] = y[b, h, p, :] turned by -a.  Same rules; with perm, rows of x
+ * that no entry names are left as they were. */
+sparge_status_t sparge_rope_inverse(const sparge_rope_t* p, const void* y, void* x,
+                                    const int32_t* pos, const double* inv_freq,
+                                    const int32_t* axis, const int32_t* perm,
+                                    cudaStream_t stream);
 
 /* Synchronises the stream and returns the status word that kernels write to
  * the workspace (SPARGE_OK, SPARGE_ETIMEOUT or SPARGE_ERANGE), then clears it.

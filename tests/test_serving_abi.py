@@ -1,0 +1,105 @@
+"""The entry points around the prompt pass reject bad arguments on the host
+before touching the GPU, and their host-side helpers give what they say.  No
+GPU needed: no call here reaches a CUDA runtime function."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def native():
+    from free_block_sparse_predict_b200 import build
+    build.build()
+    from free_block_sparse_predict_b200 import _native
+    return _native
+
+
+P = lambda x: ctypes.c_void_p(x)
+FAR = [P(0x10000000 * (i + 1)) for i in range(16)]
+
+
+# ----------------------------------------------------------------------------
+# rotary positions
+# ----------------------------------------------------------------------------
+
+def _rope(native, **kw):
+    a = dict(B=2, H=4, N=100, d=64, rot=64, axes=3, interleaved=0, dtype=1,
+             x_stride=(25600, 6400, 64), y_stride=(25600, 6400, 64), pos_stride=0)
+    a.update(kw)
+    return native.SpargeRope(*a.values())
+
+
+def _call(native, p, x=FAR[0], y=FAR[1], pos=FAR[2], f=FAR[3], ax=FAR[4], perm=None, inverse=False):
+    L = native.lib()
+    ref = ctypes.byref(p) if p is not None else None
+    if inverse:
+        return L.sparge_rope_inverse(ref, y, x, pos, f, ax, perm, None)
+    return L.sparge_rope_apply(ref, x, y, pos, f, ax, perm, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=-1), 1), (dict(H=-1), 1), (dict(N=-2), 1), (dict(d=0), 1), (dict(axes=0), 1),
+    (dict(rot=0), 1), (dict(rot=66), 1), (dict(rot=31), 1), (dict(interleaved=2), 1),
+    (dict(dtype=3), 1), (dict(pos_stride=-1), 1),
+    (dict(d=68, rot=64), 2),                                  # 136-byte rows
+    (dict(rot=24), 2),                                        # 48 bytes turn: not two equal vectors
+    (dict(x_stride=(25600, 6400, 68)), 2),                    # 136-byte steps
+    (dict(x_stride=(25600, -6400, 64)), 1),
+    (dict(y_stride=(25600, 0, 64)), 1),                       # heads written on top of one another
+    (dict(y_stride=(25600, 6400, 32)), 1),                    # half rows shared
+    (dict(y_stride=(6400, 6400, 64)), 1),                     # batch 1 on head 1
+    (dict(x_stride=(1 << 57, 1 << 57, 1 << 57), N=1 << 20), 1),
+])
+def test_rope_refusals(native, kw, code):
+    assert _call(native, _rope(native, **kw)) == code
+
+
+def test_rope_inverse_checks_what_it_writes(native):
+    shared = (25600, 0, 64)
+    assert _call(native, _rope(native, x_stride=shared), inverse=True) == 1
+    assert _call(native, _rope(native, y_stride=shared)) == 1
+
+
+def test_rope_pointers_and_overlap(native):
+    p = _rope(native)
+    assert _call(native, None) == 1
+    for name in ("x", "y", "pos", "f", "ax"):
+        assert _call(native, p, **{name: None}) == 1
+    assert _call(native, p, x=P(0x10000008)) == 1
+    assert _call(native, p, f=P(0x10000004)) == 1
+    assert _call(native, p, perm=P(0x10000002)) == 1
+    n = 2 * 4 * 100 * 64 * 2
+    assert _call(native, p, y=P(FAR[0].value + n - 16)) == 1            # the last row's end
+    assert _call(native, p, x=FAR[0], y=FAR[0], perm=FAR[5]) == 1       # in place needs no table
+    q = _rope(native, y_stride=(6400, 12800, 64))
+    assert _call(native, q, x=FAR[0], y=FAR[0]) == 1                    # in place, other strides
+
+
+@pytest.mark.parametrize("kw", [dict(B=0), dict(H=0), dict(N=0)])
+def test_rope_of_nothing(native, kw):
+    assert _call(native, _rope(native, **kw), x=None, y=None, pos=None) == 0
+
+
+def test_rope_frequencies():
+    from free_block_sparse_predict_b200 import rope_frequencies
+    f, a = rope_frequencies((2, 3, 0, 1), theta=100.0, device="cpu")
+    assert f.dtype == torch.float64 and a.dtype == torch.int32
+    want = [1.0, 0.1, 1.0, 100 ** (-1 / 3), 100 ** (-2 / 3), 1.0]
+    assert all(math.isclose(x, y, rel_tol=1e-14) for x, y in zip(f.tolist(), want))
+    assert a.tolist() == [0, 0, 1, 1, 1, 3]
+    f, _ = rope_frequencies((1, 3), theta=16.0, joint=True, device="cpu")
+    assert all(math.isclose(x, y, rel_tol=1e-14) for x, y in zip(f.tolist(), [1, .5, .25, .125]))
+
+
+def test_grid_positions():
+    from free_block_sparse_predict_b200 import SpargeError, grid_positions
+    p = grid_positions(2 + 2 * 3 * 4 + 3, 2, 2, 3, 4, device="cpu")
+    assert p.shape == (3, 29) and p.dtype == torch.int32
+    assert p[:, :2].tolist() == [[0, 1]] * 3
+    assert p[:, 2].tolist() == [2, 2, 2] and p[:, 2 + 13].tolist() == [3, 2, 3]
+    assert p[:, 25].tolist() == [3, 4, 5]
+    assert p[:, 26:].tolist() == [[6, 7, 8]] * 3
+    with pytest.raises(SpargeError):
+        grid_positions(10, 3, 2, 2, 2, device="cpu")
