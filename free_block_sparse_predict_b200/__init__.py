@@ -19,8 +19,8 @@ import torch
 
 from ._native import (SPARGE_BF16, SPARGE_F16, SPARGE_F32, SpargeError, SpargeParams,
                       SpargeStats, lib, lib_path)
-from .serving import (Rope, grid_positions, rope_frequencies, sparge_rope_apply,
-                      sparge_rope_inverse)
+from .serving import (Rope, grid_positions, rope_frequencies, sparge_kv_plan,
+                      sparge_rope_apply, sparge_rope_inverse)
 
 __all__ = [
     "SpargeError", "SpargeParams", "SpargeStats", "make_params", "lib_path",
@@ -30,6 +30,7 @@ __all__ = [
     "sparge_mask_compact", "sparge_attn_fwd", "sparge_device_status",
     "sparge_selftest_wait_timeout", "sparge_status_string",
     "Rope", "rope_frequencies", "grid_positions", "sparge_rope_apply", "sparge_rope_inverse",
+    "sparge_kv_plan",
     "workspace", "predict_outputs", "sparge_forward",
 ]
 

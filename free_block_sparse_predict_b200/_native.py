@@ -60,6 +60,7 @@ SIGNATURES = {
     "sparge_attn_fwd": (ctypes.c_int, [_P, _V, _V, _V, _V, _V, _V, _V, _S, _V, _V]),
     "sparge_rope_apply": (ctypes.c_int, [_R, _V, _V, _V, _V, _V, _V, _V]),
     "sparge_rope_inverse": (ctypes.c_int, [_R, _V, _V, _V, _V, _V, _V, _V]),
+    "sparge_kv_plan": (ctypes.c_int, [_I] * 5 + [_V] * 11),
     "sparge_device_status": (ctypes.c_int, [_V, _V]),
     "sparge_selftest_wait_timeout": (ctypes.c_int, [_V, _V]),
     "sparge_status_string": (ctypes.c_char_p, [ctypes.c_int]),

@@ -122,4 +122,49 @@ sparge_status_t sparge_rope_inverse(const sparge_rope_t* p, const void* y, void*
   return rope_common(p, y, x, pos, inv_freq, axis, perm, true, stream);
 }
 
+sparge_status_t sparge_kv_plan(int32_t R, int32_t page_size, int32_t max_pages,
+                               int32_t num_pages, int32_t max_tokens, const int32_t* new_len,
+                               const int32_t* seq_len, int32_t* block_table,
+                               int32_t* free_pages, const int32_t* free_count,
+                               int32_t* seq_len_out, int32_t* free_count_out, int32_t* cu_new,
+                               int32_t* slot_map, int32_t* admitted, cudaStream_t stream) {
+  if (R < 0 || page_size < 1 || max_pages < 0 || num_pages < 0 || max_tokens < 0)
+    return SPARGE_EINVAL;
+  if (R > kMaxPlanRequests || int64_t(num_pages) * page_size > INT32_MAX ||
+      int64_t(max_pages) * page_size > INT32_MAX)
+    return SPARGE_EUNSUPPORTED;
+  // what has no elements may be NULL
+  if (free_count == nullptr || free_count_out == nullptr || cu_new == nullptr) return SPARGE_EINVAL;
+  if (R > 0 && (new_len == nullptr || seq_len == nullptr || seq_len_out == nullptr ||
+                admitted == nullptr || (max_pages > 0 && block_table == nullptr)))
+    return SPARGE_EINVAL;
+  if ((num_pages > 0 && free_pages == nullptr) || (max_tokens > 0 && slot_map == nullptr))
+    return SPARGE_EINVAL;
+  const void* all[] = {new_len, seq_len, block_table, free_pages, free_count, seq_len_out,
+                       free_count_out, cu_new, slot_map, admitted};
+  for (const void* x : all)
+    if (!aligned(x, 4)) return SPARGE_EINVAL;
+  // what is written, apart from the two that may be their own inputs, meets nothing else
+  const int64_t r4 = 4 * int64_t(R);
+  const int64_t bytes[] = {r4, r4, r4 * max_pages, 4 * int64_t(num_pages), 4, r4, 4, r4 + 4,
+                           4 * int64_t(max_tokens), r4};
+  for (int i = 2; i < 10; ++i) {
+    if (i == 4) continue;
+    for (int j = 0; j < 10; ++j) {
+      if (j == i || bytes[i] == 0 || bytes[j] == 0) continue;
+      if (((i == 5 && j == 1) || (i == 6 && j == 4) || (i == 1 && j == 5) || (i == 4 && j == 6)) &&
+          all[i] == all[j])
+        continue;
+      if (overlap(all[i], bytes[i], all[j], bytes[j])) return SPARGE_EINVAL;
+    }
+  }
+  DeviceScope dev;
+  const sparge_status_t st = dev.enter(cu_new);
+  if (st != SPARGE_OK) return st;
+  const KvPlanArgs a{R, page_size, max_pages, num_pages, max_tokens, new_len, seq_len,
+                     block_table, free_pages, free_count, seq_len_out, free_count_out, cu_new,
+                     slot_map, admitted};
+  return from_cuda(launch_kv_plan(a, stream));
+}
+
 }  // extern "C"

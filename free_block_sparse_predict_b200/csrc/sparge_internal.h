@@ -145,6 +145,23 @@ cudaError_t launch_rope(const sparge_rope_t& p, const void* src, const int64_t* 
                         const double* inv_freq, const int32_t* axis, const int32_t* perm,
                         bool inverse, cudaStream_t s);
 
+// ------------------------------------------------------------- kv_plan.cu
+constexpr int kMaxPlanRequests = 4096;
+struct KvPlanArgs {  // as sparge_kv_plan's arguments
+  int32_t R, page_size, max_pages, num_pages, max_tokens;
+  const int32_t* new_len;
+  const int32_t* seq_len;
+  int32_t* block_table;
+  int32_t* free_pages;
+  const int32_t* free_count;
+  int32_t* seq_len_out;
+  int32_t* free_count_out;
+  int32_t* cu_new;
+  int32_t* slot_map;
+  int32_t* admitted;
+};
+cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t s);
+
 // ------------------------------------------------------------- attn_sm100.cu
 struct AttnPtrs {
   const void* q;        // io dtype, or int8 codes with qk_int8

@@ -1,5 +1,5 @@
 """Binding of the entry points around the prompt pass (include/sparge.h): rotary
-positions with several axes.
+positions with several axes, and the bookkeeping of a paged cache.
 
 As in the package's main module, every ``sparge_*`` function has the name of the
 C entry point it wraps and only checks and marshals arguments; a call runs on the
@@ -15,7 +15,7 @@ import torch
 from ._native import (SPARGE_BF16, SPARGE_F16, SPARGE_F32, SpargeError, SpargeRope, lib)
 
 __all__ = ["Rope", "rope_frequencies", "grid_positions", "sparge_rope_apply",
-           "sparge_rope_inverse"]
+           "sparge_rope_inverse", "sparge_kv_plan"]
 
 _DT = {torch.float16: SPARGE_F16, torch.bfloat16: SPARGE_BF16, torch.float32: SPARGE_F32}
 
@@ -140,3 +140,29 @@ def sparge_rope_inverse(y, x, pos, inv_freq, axis, perm: Optional[torch.Tensor] 
                         interleaved: bool = False, stream=None) -> None:
     """x[b, h, s] = y[b, h, p] turned back: the inverse of sparge_rope_apply and its gradient."""
     _rope(True, x, y, pos, inv_freq, axis, perm, interleaved, stream)
+
+
+# ----------------------------------------------------------------------------
+# pages
+# ----------------------------------------------------------------------------
+
+def sparge_kv_plan(new_len, seq_len, block_table, free_pages, free_count, page_size: int,
+                   seq_len_out, free_count_out, cu_new, slot_map, admitted, stream=None) -> None:
+    """One step of a paged cache's bookkeeping; every tensor is int32.
+
+    new_len, seq_len, seq_len_out, admitted [R]; block_table [R, max_pages]; free_pages
+    [num_pages]; free_count, free_count_out [1]; cu_new [R + 1]; slot_map [max_tokens].
+    seq_len_out may be seq_len and free_count_out may be free_count."""
+    dev = _device(cu_new, "cu_new")
+    if block_table.dim() != 2:
+        raise _bad("block_table: expected [R, max_pages]")
+    (R, width), i32 = block_table.shape, torch.int32
+    pages, tokens = free_pages.numel(), slot_map.numel()
+    _check(lib().sparge_kv_plan(
+        R, page_size, width, pages, tokens, _flat(new_len, "new_len", R, i32, dev),
+        _flat(seq_len, "seq_len", R, i32, dev), _flat(block_table, "block_table", 0, i32, dev),
+        _flat(free_pages, "free_pages", 0, i32, dev), _flat(free_count, "free_count", 1, i32, dev),
+        _flat(seq_len_out, "seq_len_out", R, i32, dev),
+        _flat(free_count_out, "free_count_out", 1, i32, dev),
+        _flat(cu_new, "cu_new", R + 1, i32, dev), _flat(slot_map, "slot_map", 0, i32, dev),
+        _flat(admitted, "admitted", R, i32, dev), _stream(stream, dev)))

@@ -254,6 +254,36 @@ sparge_status_t sparge_rope_inverse(const sparge_rope_t* p, const void* y, void*
                                     const int32_t* axis, const int32_t* perm,
                                     cudaStream_t stream);
 
+/* One step of a paged cache's bookkeeping, on the device: which requests get the pages
+ * they need, their block tables, and the slot of every new token.
+ *   new_len      int32 [R]: tokens that request r brings; 0: none; < 0: it has ended
+ *   seq_len      int32 [R]: tokens it has in the cache so far
+ *   block_table  int32 [R, max_pages], in and out: entry j is the page of tokens
+ *                [j * page_size, (j + 1) * page_size)
+ *   free_pages   int32 [num_pages], in and out: a stack of free page numbers
+ *   free_count   int32 [1]: its height
+ * In this order: the pages of ended requests are pushed (request by request, each in table
+ * order); then requests with new tokens are admitted in order.  A request is admitted when
+ * its tokens fit its table row and max_tokens slots and the pages it needs, together with
+ * those of every earlier such request, are there; one that needs no new page is always
+ * admitted then.  Pages are popped from the top, request by request.
+ *   seq_len_out, free_count_out  the new values (may be seq_len and free_count themselves)
+ *   cu_new       int32 [R + 1]: where each request's new tokens start (cu_q of the attention)
+ *   slot_map     int32 [max_tokens]: page * page_size + offset of new token t; -1 for a
+ *                token of a request that was not admitted and behind the last token
+ *   admitted     int32 [R]: 0 for a request whose new tokens found no room, else 1
+ * A request that is not admitted keeps its length and its pages.  Lengths outside
+ * [0, max_pages * page_size] are taken as the nearer end, a height outside [0, num_pages]
+ * likewise; what would be pushed past num_pages is dropped.
+ * The outputs may not overlap one another or the inputs, apart from the two named above.
+ * SPARGE_EUNSUPPORTED: R > 4096, or num_pages or max_pages times page_size >= 2^31. */
+sparge_status_t sparge_kv_plan(int32_t R, int32_t page_size, int32_t max_pages,
+                               int32_t num_pages, int32_t max_tokens, const int32_t* new_len,
+                               const int32_t* seq_len, int32_t* block_table,
+                               int32_t* free_pages, const int32_t* free_count,
+                               int32_t* seq_len_out, int32_t* free_count_out, int32_t* cu_new,
+                               int32_t* slot_map, int32_t* admitted, cudaStream_t stream);
+
 /* Synchronises the stream and returns the status word that kernels write to
  * the workspace (SPARGE_OK, SPARGE_ETIMEOUT or SPARGE_ERANGE), then clears it.
  * ws: the workspace of sparge_predict_mask / sparge_attn_fwd. */

@@ -103,3 +103,41 @@ def test_grid_positions():
     assert p[:, 26:].tolist() == [[6, 7, 8]] * 3
     with pytest.raises(SpargeError):
         grid_positions(10, 3, 2, 2, 2, device="cpu")
+
+
+# ----------------------------------------------------------------------------
+# pages
+# ----------------------------------------------------------------------------
+
+def _plan(native, R=4, P=16, width=8, pages=100, tokens=50, ptrs=None, **swap):
+    names = ["new", "len", "table", "free", "count", "len_out", "count_out", "cu", "slots", "adm"]
+    a = dict(zip(names, ptrs or FAR))
+    a.update(swap)
+    return native.lib().sparge_kv_plan(R, P, width, pages, tokens, *[a[n] for n in names], None)
+
+
+def test_plan_refusals(native):
+    for kw in (dict(R=-1), dict(P=0), dict(width=-1), dict(pages=-1), dict(tokens=-1)):
+        assert _plan(native, **kw) == 1
+    assert _plan(native, R=4097) == 2
+    assert _plan(native, pages=1 << 27) == 2 and _plan(native, width=1 << 27) == 2
+    for name in ("new", "len", "table", "free", "count", "len_out", "count_out", "cu", "slots",
+                 "adm"):
+        assert _plan(native, **{name: None}) == 1, name
+        assert _plan(native, **{name: P(0x90000002)}) == 1, name
+    assert _plan(native, len_out=FAR[0]) == 1                     # over new_len
+    assert _plan(native, adm=P(FAR[8].value + 4 * 49)) == 1       # over the last slot
+    assert _plan(native, len_out=P(FAR[1].value + 4)) == 1        # beside itself
+
+
+def test_plan_oracle_by_hand():
+    """The reference the GPU tests use, on a step small enough to follow."""
+    import numpy as np
+    from serving_common import plan_oracle
+    table = np.array([[5, -1], [6, 7], [-1, -1]])
+    got = plan_oracle([1, -1, 3], [4, 8, 0], table, np.array([9, 8, 0, 0]), 1, 4, 6)
+    # 6, 7 come back on top of 9; request 0 takes 7, request 2 takes 6
+    assert got["free"].tolist() == [9, 6, 7, 0] and got["count"] == 1
+    assert got["table"].tolist() == [[5, 7], [6, 7], [6, -1]]
+    assert got["slots"].tolist() == [28, 24, 25, 26, -1, -1]
+    assert got["cu"].tolist() == [0, 1, 1, 4] and got["length"].tolist() == [5, 0, 3]
