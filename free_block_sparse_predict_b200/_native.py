@@ -40,11 +40,18 @@ class SpargeRope(ctypes.Structure):
                 ("pos_stride", ctypes.c_int64)]
 
 
+class SpargeKv4(ctypes.Structure):
+    _fields_ = [("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32)]
+
+
 _P = ctypes.POINTER(SpargeParams)
+_K = ctypes.POINTER(SpargeKv4)
 _R = ctypes.POINTER(SpargeRope)
 _V = ctypes.c_void_p
 _I = ctypes.c_int32
 _S = ctypes.c_size_t
+_D = ctypes.POINTER(ctypes.c_int64)
 
 SIGNATURES = {
     "sparge_workspace_bytes": (_S, [_P]),
@@ -61,6 +68,9 @@ SIGNATURES = {
     "sparge_rope_apply": (ctypes.c_int, [_R, _V, _V, _V, _V, _V, _V, _V]),
     "sparge_rope_inverse": (ctypes.c_int, [_R, _V, _V, _V, _V, _V, _V, _V]),
     "sparge_kv_plan": (ctypes.c_int, [_I] * 5 + [_V] * 11),
+    "sparge_kv4_bytes": (_S, [_K]),
+    "sparge_kv4_append": (ctypes.c_int, [_K, _I, _V, _D, _V, _D, ctypes.c_int, _V, _V, _V, _V]),
+    "sparge_kv4_read": (ctypes.c_int, [_K, _I, _V, _V, _V, _D, _V, _D, ctypes.c_int, _V]),
     "sparge_device_status": (ctypes.c_int, [_V, _V]),
     "sparge_selftest_wait_timeout": (ctypes.c_int, [_V, _V]),
     "sparge_status_string": (ctypes.c_char_p, [ctypes.c_int]),

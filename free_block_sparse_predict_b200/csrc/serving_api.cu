@@ -57,6 +57,35 @@ bool disjoint(Rows r) {
   return true;
 }
 
+// SPARGE_OK, SPARGE_EINVAL or SPARGE_EUNSUPPORTED for a cache's shape.
+sparge_status_t check_kv4(const sparge_kv4_t* c) {
+  if (c == nullptr || c->Hkv < 1 || c->d < 1 || c->group < 1 || c->page_size < 1 ||
+      c->num_pages < 0)
+    return SPARGE_EINVAL;
+  if (c->page_size % 16 != 0) return SPARGE_EINVAL;
+  if (c->d != 64 && c->d != 128) return SPARGE_EUNSUPPORTED;
+  if (c->group != 32 && c->group != 64 && c->group != 128) return SPARGE_EUNSUPPORTED;
+  if (c->group > c->d) return SPARGE_EINVAL;
+  if (c->Hkv > 65535 || int64_t(c->num_pages) * c->page_size > INT32_MAX ||
+      int64_t(c->num_pages) * c->page_size / 16 * c->Hkv > INT32_MAX)
+    return SPARGE_EUNSUPPORTED;
+  return SPARGE_OK;
+}
+
+// Token and head strides of a [T, Hkv, d] tensor, in bytes.
+sparge_status_t row_strides(const int64_t* st, int64_t T, int64_t H, int64_t row, int64_t es,
+                            Rows* r) {
+  *r = Rows{{T, H, 1}, {0, 0, 0}, row};
+  if (st == nullptr) return SPARGE_EINVAL;
+  for (int i = 0; i < 2; ++i) {
+    if (r->ext[i] <= 1) continue;
+    if (st[i] < 0 || st[i] > (int64_t(1) << 58)) return SPARGE_EINVAL;
+    r->stride[i] = st[i] * es;
+    if (r->stride[i] % 16 != 0) return SPARGE_EUNSUPPORTED;
+  }
+  return extent(*r) < 0 ? SPARGE_EINVAL : SPARGE_OK;
+}
+
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + uintptr_t(nb) && y < x + uintptr_t(na);
@@ -165,6 +194,62 @@ sparge_status_t sparge_kv_plan(int32_t R, int32_t page_size, int32_t max_pages,
                      block_table, free_pages, free_count, seq_len_out, free_count_out, cu_new,
                      slot_map, admitted};
   return from_cuda(launch_kv_plan(a, stream));
+}
+
+size_t sparge_kv4_bytes(const sparge_kv4_t* c) {
+  if (check_kv4(c) != SPARGE_OK) return 0;
+  return size_t(c->num_pages) * c->Hkv * c->page_size * (c->d + 4 * (c->d / c->group));
+}
+
+static sparge_status_t cache_common(bool read, const sparge_kv4_t* c, int32_t T, void* k,
+                                    const int64_t* k_stride, void* v, const int64_t* v_stride,
+                                    sparge_dtype_t dtype, const int32_t* slot_map, void* cache,
+                                    int32_t* status, cudaStream_t stream) {
+  sparge_status_t st = check_kv4(c);
+  if (st != SPARGE_OK) return st;
+  if (T < 0 || !is_dtype(dtype)) return SPARGE_EINVAL;
+  if (!read && dtype == SPARGE_F32) return SPARGE_EUNSUPPORTED;
+  if (T == 0 || c->num_pages == 0) return SPARGE_OK;
+  if (slot_map == nullptr || cache == nullptr || !aligned(slot_map, 4) || !aligned(cache, 16) ||
+      !aligned(status, 4) || !aligned(k, 16) || !aligned(v, 16))
+    return SPARGE_EINVAL;
+  if (!read && (k == nullptr || v == nullptr)) return SPARGE_EINVAL;
+  if (k == nullptr && v == nullptr) return SPARGE_OK;
+  const int64_t es = elem_size(dtype), row = c->d * es;
+  const int64_t cache_bytes = int64_t(sparge_kv4_bytes(c));
+  Rows r[2];
+  void* const p[2] = {k, v};
+  for (int i = 0; i < 2; ++i) {
+    r[i] = Rows{{T, c->Hkv, 1}, {0, 0, 0}, row};
+    if (p[i] == nullptr) continue;
+    if ((st = row_strides(i == 0 ? k_stride : v_stride, T, c->Hkv, row, es, &r[i])) != SPARGE_OK)
+      return st;
+    if (overlap(p[i], extent(r[i]), cache, cache_bytes)) return SPARGE_EINVAL;
+    if (read && (!disjoint(r[i]) || overlap(p[i], extent(r[i]), slot_map, 4 * int64_t(T))))
+      return SPARGE_EINVAL;
+  }
+  if (!read && overlap(slot_map, 4 * int64_t(T), cache, cache_bytes)) return SPARGE_EINVAL;
+  DeviceScope dev;
+  if ((st = dev.enter(cache)) != SPARGE_OK) return st;
+  return from_cuda(launch_kv4_cache(*c, read, T, k, r[0].stride, v, r[1].stride, dtype, slot_map,
+                                    cache, status, stream));
+}
+
+sparge_status_t sparge_kv4_append(const sparge_kv4_t* c, int32_t T, const void* k,
+                                  const int64_t k_stride[2], const void* v,
+                                  const int64_t v_stride[2], sparge_dtype_t dtype,
+                                  const int32_t* slot_map, void* cache, int32_t* status,
+                                  cudaStream_t stream) {
+  return cache_common(false, c, T, const_cast<void*>(k), k_stride, const_cast<void*>(v), v_stride,
+                      dtype, slot_map, cache, status, stream);
+}
+
+sparge_status_t sparge_kv4_read(const sparge_kv4_t* c, int32_t T, const void* cache,
+                                const int32_t* slot_map, void* k, const int64_t k_stride[2],
+                                void* v, const int64_t v_stride[2], sparge_dtype_t dtype,
+                                cudaStream_t stream) {
+  return cache_common(true, c, T, k, k_stride, v, v_stride, dtype, slot_map,
+                      const_cast<void*>(cache), nullptr, stream);
 }
 
 }  // extern "C"

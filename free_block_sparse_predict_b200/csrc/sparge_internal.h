@@ -162,6 +162,13 @@ struct KvPlanArgs {  // as sparge_kv_plan's arguments
 };
 cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t s);
 
+// ------------------------------------------------------------- kv4_cache.cu
+// strides in bytes, tokens / heads; append when not read
+cudaError_t launch_kv4_cache(const sparge_kv4_t& c, bool read, int32_t T, void* k,
+                             const int64_t* ks, void* v, const int64_t* vs,
+                             sparge_dtype_t dtype, const int32_t* slots, void* cache,
+                             int32_t* status, cudaStream_t s);
+
 // ------------------------------------------------------------- attn_sm100.cu
 struct AttnPtrs {
   const void* q;        // io dtype, or int8 codes with qk_int8

@@ -1,5 +1,5 @@
 """Binding of the entry points around the prompt pass (include/sparge.h): rotary
-positions with several axes, and the bookkeeping of a paged cache.
+positions with several axes, the bookkeeping of a paged cache, and the cache in 4 bits.
 
 As in the package's main module, every ``sparge_*`` function has the name of the
 C entry point it wraps and only checks and marshals arguments; a call runs on the
@@ -12,10 +12,12 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from ._native import (SPARGE_BF16, SPARGE_F16, SPARGE_F32, SpargeError, SpargeRope, lib)
+from ._native import (SPARGE_BF16, SPARGE_F16, SPARGE_F32, SpargeError, SpargeKv4, SpargeRope,
+                      lib)
 
 __all__ = ["Rope", "rope_frequencies", "grid_positions", "sparge_rope_apply",
-           "sparge_rope_inverse", "sparge_kv_plan"]
+           "sparge_rope_inverse", "sparge_kv_plan", "SpargeKv4", "make_kv4", "kv4_cache",
+           "sparge_kv4_bytes", "sparge_kv4_append", "sparge_kv4_read"]
 
 _DT = {torch.float16: SPARGE_F16, torch.bfloat16: SPARGE_BF16, torch.float32: SPARGE_F32}
 
@@ -166,3 +168,86 @@ def sparge_kv_plan(new_len, seq_len, block_table, free_pages, free_count, page_s
         _flat(free_count_out, "free_count_out", 1, i32, dev),
         _flat(cu_new, "cu_new", R + 1, i32, dev), _flat(slot_map, "slot_map", 0, i32, dev),
         _flat(admitted, "admitted", R, i32, dev), _stream(stream, dev)))
+
+
+# ----------------------------------------------------------------------------
+# the cache in 4 bits
+# ----------------------------------------------------------------------------
+
+def make_kv4(Hkv: int, d: int, group: int, page_size: int, num_pages: int) -> SpargeKv4:
+    """Shape of a 4-bit cache: KV heads, channels, channels per scale, tokens per page, pages."""
+    return SpargeKv4(Hkv, d, group, page_size, num_pages)
+
+
+def sparge_kv4_bytes(c: SpargeKv4) -> int:
+    return int(lib().sparge_kv4_bytes(ctypes.byref(c)))
+
+
+def kv4_cache(c: SpargeKv4, device="cuda") -> torch.Tensor:
+    """Memory for the cache: uint8 [num_pages, Hkv, page_size / 16, bytes of a 16-token tile]."""
+    if sparge_kv4_bytes(c) == 0:
+        raise _bad("invalid cache parameters")
+    tile = 16 * (c.d + 4 * (c.d // c.group))
+    return torch.empty((c.num_pages, c.Hkv, c.page_size // 16, tile), dtype=torch.uint8,
+                       device=device)
+
+
+_I64x2 = ctypes.c_int64 * 2
+
+
+def _rows(x, name, c, T, dev, dtypes):
+    """Address and token / head strides of a [T, Hkv, d] tensor."""
+    if x.device != dev:
+        raise _bad(f"{name}: expected a tensor on {dev}, got {x.device}")
+    if x.dim() != 3 or tuple(x.shape) != (T, c.Hkv, c.d):
+        raise _bad(f"{name}: expected [{T}, {c.Hkv}, {c.d}], got {list(x.shape)}")
+    if x.dtype not in dtypes:
+        raise _bad(f"{name}: got {x.dtype}")
+    s = x.stride()
+    if s[2] != 1:
+        raise _bad(f"{name}: the channels have to be contiguous")
+    return x.data_ptr(), _I64x2(s[0], s[1])
+
+
+def _cache_ptr(c, cache) -> int:
+    need = sparge_kv4_bytes(c)
+    if need == 0 and c.num_pages != 0:
+        raise _bad("invalid cache parameters")
+    if cache.dtype != torch.uint8 or not cache.is_contiguous() or cache.numel() < need:
+        raise _bad(f"cache: expected {need} contiguous bytes")
+    return cache.data_ptr()
+
+
+def sparge_kv4_append(c: SpargeKv4, k, v, slot_map, cache, status=None, stream=None) -> None:
+    """Rows of k and v [T, Hkv, d] (any token and head strides) into the slots slot_map [T];
+    slots outside the cache are skipped.  status: an int32 tensor, or a workspace, whose first
+    word receives SPARGE_ERANGE (6) when a scale was saturated."""
+    dev, T = _device(cache, "cache"), slot_map.numel()
+    pc = _cache_ptr(c, cache)
+    pk, sk = _rows(k, "k", c, T, dev, (torch.float16, torch.bfloat16))
+    pv, sv = _rows(v, "v", c, T, dev, (k.dtype,))
+    if status is not None:
+        if status.device != dev or status.numel() * status.element_size() < 4:
+            raise _bad(f"status: expected 4 bytes on {dev}")
+        status = status.data_ptr()
+    _check(lib().sparge_kv4_append(ctypes.byref(c), T, pk, sk, pv, sv, _DT[k.dtype],
+                                   _flat(slot_map, "slot_map", T, torch.int32, dev), pc, status,
+                                   _stream(stream, dev)))
+
+
+def sparge_kv4_read(c: SpargeKv4, cache, slot_map, k, v, stream=None) -> None:
+    """The values that the slots slot_map [T] hold, into rows of k and v [T, Hkv, d] (16-bit or
+    float32; either may be None); rows whose slot is outside the cache stay as they were."""
+    dev, T = _device(cache, "cache"), slot_map.numel()
+    pc = _cache_ptr(c, cache)
+    pk = pv = sk = sv = None
+    first = k if k is not None else v
+    if first is None:
+        return
+    if k is not None:
+        pk, sk = _rows(k, "k", c, T, dev, _DT)
+    if v is not None:
+        pv, sv = _rows(v, "v", c, T, dev, (first.dtype,) if first.dtype in _DT else ())
+    _check(lib().sparge_kv4_read(ctypes.byref(c), T, pc,
+                                 _flat(slot_map, "slot_map", T, torch.int32, dev), pk, sk, pv, sv,
+                                 _DT[first.dtype], _stream(stream, dev)))

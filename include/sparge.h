@@ -284,6 +284,52 @@ sparge_status_t sparge_kv_plan(int32_t R, int32_t page_size, int32_t max_pages,
                                int32_t* seq_len_out, int32_t* free_count_out, int32_t* cu_new,
                                int32_t* slot_map, int32_t* admitted, cudaStream_t stream);
 
+/* A paged cache of K and V in 4 bits.  Every (token, KV head) row of d channels is cut into
+ * d / group groups; each has one fp16 scale s = absmax / 7 (the quotient in float32, rounded
+ * to fp16) and per channel the code c = round-half-even(x / s) of the IEEE float32 quotient,
+ * clamped to [-7, 7] and held as c + 8.  The value is c * s.  A group whose s is 0 has codes
+ * 0; a group with a NaN has s = NaN; s above 16376 is saturated (SPARGE_ERANGE), so that a
+ * softmax weight times s stays in fp16.
+ * Memory: uint8 [num_pages, Hkv, page_size / 16, tile], a tile holding 16 tokens:
+ *   8d bytes      codes of K, token rows of d/2 bytes: byte b of 32-bit word (t, j), t < 4,
+ *                 j < d/32, holds channels 32j + 8t + e, e = (0,2), (4,6), (1,3), (5,7) for
+ *                 b = 0..3, the first in the low half
+ *   8d bytes      codes of V, [d/64 w][8 g][16 p][4 i]: channels 64w + 16i + 2g (low half)
+ *                 and 64w + 16i + 2g + 1 of the token k with p = 4((k%8)/2) + 2(k/8) + k%2
+ *   64d/group     scales, fp16 [16 tokens][d/group of K, d/group of V]
+ * which is the order in which the tensor-core fragments take them.  A token's bytes are its
+ * own, so writes of different tokens never meet. */
+typedef struct {
+  int32_t Hkv, d;      /* d in {64, 128}                                      */
+  int32_t group;       /* channels per scale: 32, 64 or 128, at most d        */
+  int32_t page_size;   /* tokens per page: a multiple of 16                   */
+  int32_t num_pages;   /* num_pages * page_size < 2^31                        */
+} sparge_kv4_t;
+
+/* Bytes of the cache; 0 for invalid or unsupported parameters.  Its base must be 16-byte
+ * aligned.  No initial contents are needed: only written tokens are ever used. */
+size_t sparge_kv4_bytes(const sparge_kv4_t* c);
+
+/* Writes T tokens: row t of k and v goes to slot slot_map[t] = page * page_size + offset;
+ * rows whose slot lies outside [0, num_pages * page_size) are skipped.  If two rows name one
+ * slot, each byte of it is one of the two's and which is unspecified.
+ * k, v: [T, Hkv, d] of dtype (16-bit), channels contiguous; *_stride: elements between tokens
+ * and heads, multiples of 16 bytes.  status: nullable device int32 that receives
+ * SPARGE_ERANGE (the first word of a workspace will do). */
+sparge_status_t sparge_kv4_append(const sparge_kv4_t* c, int32_t T, const void* k,
+                                  const int64_t k_stride[2], const void* v,
+                                  const int64_t v_stride[2], sparge_dtype_t dtype,
+                                  const int32_t* slot_map, void* cache, int32_t* status,
+                                  cudaStream_t stream);
+
+/* The values that T slots hold, c * s in float32 rounded once to dtype (16-bit or float32),
+ * into rows of k and v (either nullable); rows whose slot lies outside the cache are left as
+ * they were. */
+sparge_status_t sparge_kv4_read(const sparge_kv4_t* c, int32_t T, const void* cache,
+                                const int32_t* slot_map, void* k, const int64_t k_stride[2],
+                                void* v, const int64_t v_stride[2], sparge_dtype_t dtype,
+                                cudaStream_t stream);
+
 /* Synchronises the stream and returns the status word that kernels write to
  * the workspace (SPARGE_OK, SPARGE_ETIMEOUT or SPARGE_ERANGE), then clears it.
  * ws: the workspace of sparge_predict_mask / sparge_attn_fwd. */

@@ -100,3 +100,56 @@ def random_plan(rng, R, P, width, new_max, ended=0.2, spare=1.0, idle=0.1):
     free = np.full(num, -1)
     free[:count] = ids[at:at + count]
     return new, length, table, free, count, P
+
+
+# ----------------------------------------------------------------------------
+# the 4-bit cache
+# ----------------------------------------------------------------------------
+
+MAX_SCALE = np.float16(16376.0)
+
+
+def kv4_quantise(x, group):
+    """(codes int [.., d], scales fp16 [.., d/group]) of float32 rows, and whether any scale
+    was saturated."""
+    x = np.asarray(x, np.float32)
+    y = x.reshape(*x.shape[:-1], -1, group)
+    with np.errstate(all="ignore"):
+        s = np.abs(y).max(-1) / np.float32(7)                   # a NaN stays one
+        high = s > np.float32(MAX_SCALE)
+        s = np.where(high, MAX_SCALE, s.astype(np.float16))
+        q = y / s.astype(np.float32)[..., None]
+        c = np.where(s[..., None] > 0, np.clip(np.rint(q), -7, 7), 0)
+    return c.astype(np.int64).reshape(x.shape), s, bool(high.any())
+
+
+def kv4_values(c, s):
+    """What codes and scales stand for, float32 (exact: 4 by 11 bits)."""
+    with np.errstate(all="ignore"):
+        y = c.reshape(*s.shape, -1).astype(np.float32) * s.astype(np.float32)[..., None]
+    return y.reshape(c.shape)
+
+
+def kv4_write(cache, slot, page_size, kc, ks, vc, vs):
+    """One token's codes [Hkv, d] and scales [Hkv, ng] into the cache's bytes
+    [pages, Hkv, page/16, tile], by the documented layout."""
+    page, tok = divmod(slot, page_size)
+    tile, k = divmod(tok, 16)
+    Hkv, d = kc.shape
+    ng = ks.shape[1]
+    for h in range(Hkv):
+        b = cache[page, h, tile]
+        for j in range(d // 32):
+            for t in range(4):
+                for n, (lo, hi) in enumerate(((0, 2), (4, 6), (1, 3), (5, 7))):
+                    at = 32 * j + 8 * t
+                    b[k * (d // 2) + (t * (d // 32) + j) * 4 + n] = \
+                        (kc[h, at + lo] + 8) | (kc[h, at + hi] + 8) << 4
+        p = 4 * ((k % 8) // 2) + 2 * (k // 8) + k % 2
+        for w in range(d // 64):
+            for g in range(8):
+                for i in range(4):
+                    at = 64 * w + 16 * i + 2 * g
+                    b[8 * d + ((w * 8 + g) * 16 + p) * 4 + i] = (vc[h, at] + 8) | (vc[h, at + 1] + 8) << 4
+        sc = np.concatenate([ks[h], vs[h]]).astype(np.float16).view(np.uint8)
+        b[16 * d + k * ng * 4:16 * d + (k + 1) * ng * 4] = sc

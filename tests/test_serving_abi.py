@@ -141,3 +141,62 @@ def test_plan_oracle_by_hand():
     assert got["table"].tolist() == [[5, 7], [6, 7], [6, -1]]
     assert got["slots"].tolist() == [28, 24, 25, 26, -1, -1]
     assert got["cu"].tolist() == [0, 1, 1, 4] and got["length"].tolist() == [5, 0, 3]
+
+
+# ----------------------------------------------------------------------------
+# the 4-bit cache
+# ----------------------------------------------------------------------------
+
+def _kv4(native, **kw):
+    a = dict(Hkv=2, d=64, group=32, page_size=16, num_pages=10)
+    a.update(kw)
+    return native.SpargeKv4(*a.values())
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(Hkv=0), 1), (dict(d=96), 2), (dict(group=16), 2), (dict(group=128), 1),
+    (dict(page_size=0), 1), (dict(page_size=24), 1), (dict(num_pages=-1), 1),
+    (dict(num_pages=1 << 28), 2), (dict(d=0), 1), (dict(Hkv=70000), 2)])
+def test_cache_shapes_refused(native, kw, code):
+    c = _kv4(native, **kw)
+    L, two = native.lib(), (ctypes.c_int64 * 2)(128, 64)
+    assert L.sparge_kv4_bytes(ctypes.byref(c)) == 0
+    assert L.sparge_kv4_append(ctypes.byref(c), 3, FAR[0], two, FAR[1], two, 1, FAR[2], FAR[3], None,
+                               None) == code
+    assert L.sparge_kv4_read(ctypes.byref(c), 3, FAR[3], FAR[2], FAR[0], two, FAR[1], two, 1,
+                             None) == code
+
+
+def test_cache_bytes(native):
+    L = native.lib()
+    assert L.sparge_kv4_bytes(ctypes.byref(_kv4(native))) == 10 * 2 * 16 * (64 + 4 * 2)
+    c = _kv4(native, d=128, group=128, page_size=64, Hkv=8)
+    assert L.sparge_kv4_bytes(ctypes.byref(c)) == 10 * 8 * 64 * (128 + 4)
+    assert L.sparge_kv4_bytes(None) == 0
+
+
+def test_cache_pointers_and_strides(native):
+    L, c = native.lib(), _kv4(native)
+    S = lambda a, b: (ctypes.c_int64 * 2)(a, b)
+
+    def append(T=3, k=FAR[0], ks=S(128, 64), v=FAR[1], vs=S(128, 64), dt=1, slots=FAR[2],
+               cache=FAR[3], status=None):
+        return L.sparge_kv4_append(ctypes.byref(c), T, k, ks, v, vs, dt, slots, cache, status, None)
+
+    def read(T=3, k=FAR[0], ks=S(128, 64), v=FAR[1], vs=S(128, 64), dt=1, slots=FAR[2],
+             cache=FAR[3]):
+        return L.sparge_kv4_read(ctypes.byref(c), T, cache, slots, k, ks, v, vs, dt, None)
+
+    assert append(T=-1) == 1 and append(T=0, k=None) == 0
+    for f in (append, read):
+        assert f(slots=None) == 1 and f(cache=None) == 1 and f(dt=5) == 1
+        assert f(cache=P(0x10000008)) == 1 and f(slots=P(0x10000002)) == 1
+        assert f(k=P(0x10000008)) == 1 and f(ks=S(-128, 64)) == 1 and f(ks=None) == 1
+        assert f(ks=S(132, 64)) == 2
+        assert f(k=FAR[3]) == 1                                   # inside the cache
+    assert append(k=None) == 1 and append(dt=2) == 2
+    assert append(status=P(0x50000002)) == 1
+    assert append(slots=P(FAR[3].value + 64)) == 1
+    assert read(k=None, v=None) == 0
+    assert read(ks=S(0, 64)) == 1 and read(ks=S(128, 32)) == 1    # rows that overlap
+    assert read(k=P(FAR[2].value - 128)) == 1                     # over the slots
