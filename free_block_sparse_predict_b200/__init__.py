@@ -19,9 +19,11 @@ import torch
 
 from ._native import (SPARGE_BF16, SPARGE_F16, SPARGE_F32, SpargeError, SpargeParams,
                       SpargeStats, lib, lib_path)
-from .serving import (Rope, SpargeKv4, grid_positions, kv4_cache, make_kv4, rope_frequencies,
-                      sparge_kv4_append, sparge_kv4_bytes, sparge_kv4_read, sparge_kv_plan,
+from .serving import (Rope, SpargeKv4, grid_positions, kv4_cache, kv4_workspace, make_kv4,
+                      rope_frequencies, sparge_kv4_append, sparge_kv4_attn, sparge_kv4_bytes,
+                      sparge_kv4_read, sparge_kv4_workspace_bytes, sparge_kv_plan,
                       sparge_rope_apply, sparge_rope_inverse)
+
 
 __all__ = [
     "SpargeError", "SpargeParams", "SpargeStats", "make_params", "lib_path",
@@ -32,7 +34,8 @@ __all__ = [
     "sparge_selftest_wait_timeout", "sparge_status_string",
     "Rope", "rope_frequencies", "grid_positions", "sparge_rope_apply", "sparge_rope_inverse",
     "sparge_kv_plan", "SpargeKv4", "make_kv4", "kv4_cache", "sparge_kv4_bytes",
-    "sparge_kv4_append", "sparge_kv4_read",
+    "sparge_kv4_append", "sparge_kv4_read", "kv4_workspace", "sparge_kv4_workspace_bytes",
+    "sparge_kv4_attn",
     "workspace", "predict_outputs", "sparge_forward",
 ]
 

@@ -45,7 +45,16 @@ class SpargeKv4(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32)]
 
 
+class SpargeKv4Attn(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int32), ("T", ctypes.c_int32), ("Hq", ctypes.c_int32),
+                ("max_q", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("max_len", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("dtype", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64)]
+
+
 _P = ctypes.POINTER(SpargeParams)
+_A = ctypes.POINTER(SpargeKv4Attn)
 _K = ctypes.POINTER(SpargeKv4)
 _R = ctypes.POINTER(SpargeRope)
 _V = ctypes.c_void_p
@@ -71,6 +80,8 @@ SIGNATURES = {
     "sparge_kv4_bytes": (_S, [_K]),
     "sparge_kv4_append": (ctypes.c_int, [_K, _I, _V, _D, _V, _D, ctypes.c_int, _V, _V, _V, _V]),
     "sparge_kv4_read": (ctypes.c_int, [_K, _I, _V, _V, _V, _D, _V, _D, ctypes.c_int, _V]),
+    "sparge_kv4_workspace_bytes": (_S, [_K, _A]),
+    "sparge_kv4_attn": (ctypes.c_int, [_K, _A, _V, _V, _V, _V, _V, _V, _V, _V, _S, _V]),
     "sparge_device_status": (ctypes.c_int, [_V, _V]),
     "sparge_selftest_wait_timeout": (ctypes.c_int, [_V, _V]),
     "sparge_status_string": (ctypes.c_char_p, [ctypes.c_int]),

@@ -86,6 +86,24 @@ sparge_status_t row_strides(const int64_t* st, int64_t T, int64_t H, int64_t row
   return extent(*r) < 0 ? SPARGE_EINVAL : SPARGE_OK;
 }
 
+sparge_status_t check_attn(const sparge_kv4_t* c, const sparge_kv4_attn_t* a) {
+  const sparge_status_t st = check_kv4(c);
+  if (st != SPARGE_OK) return st;
+  if (a == nullptr || a->R < 0 || a->T < 0 || a->Hq < 1 || a->Hq % c->Hkv != 0 || a->max_q < 0 ||
+      a->max_pages < 0 || a->max_len < 0 || (a->causal != 0 && a->causal != 1) ||
+      !std::isfinite(a->scale) || !(a->scale > 0.f) ||
+      (a->dtype != SPARGE_F16 && a->dtype != SPARGE_BF16))
+    return SPARGE_EINVAL;
+  if (a->T > 1 && (a->q_stride < int64_t(a->Hq) * c->d || a->q_stride > (int64_t(1) << 40)))
+    return SPARGE_EINVAL;
+  if (a->T > 1 && a->q_stride % 8 != 0) return SPARGE_EUNSUPPORTED;
+  if (a->R > 65535 || int64_t(a->T) * a->Hq > INT32_MAX ||
+      int64_t(a->max_q) * a->Hq > INT32_MAX ||
+      int64_t(a->max_pages) * c->page_size > INT32_MAX - 64)
+    return SPARGE_EUNSUPPORTED;
+  return kv4_attn_fits(*c, *a) ? SPARGE_OK : SPARGE_EUNSUPPORTED;
+}
+
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + uintptr_t(nb) && y < x + uintptr_t(na);
@@ -250,6 +268,42 @@ sparge_status_t sparge_kv4_read(const sparge_kv4_t* c, int32_t T, const void* ca
                                 cudaStream_t stream) {
   return cache_common(true, c, T, k, k_stride, v, v_stride, dtype, slot_map,
                       const_cast<void*>(cache), nullptr, stream);
+}
+
+size_t sparge_kv4_workspace_bytes(const sparge_kv4_t* c, const sparge_kv4_attn_t* a) {
+  if (check_attn(c, a) != SPARGE_OK) return 0;
+  return kv4_attn_ws_bytes(*c, *a);
+}
+
+sparge_status_t sparge_kv4_attn(const sparge_kv4_t* c, const sparge_kv4_attn_t* a,
+                                const void* q, const void* cache, const int32_t* block_table,
+                                const int32_t* seq_len, const int32_t* cu_q, void* o,
+                                float* lse, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  sparge_status_t st = check_attn(c, a);
+  if (st != SPARGE_OK) return st;
+  if (a->R == 0 || a->T == 0 || a->max_q == 0) return SPARGE_OK;
+  if (q == nullptr || seq_len == nullptr || cu_q == nullptr || o == nullptr || ws == nullptr)
+    return SPARGE_EINVAL;
+  if ((a->max_pages > 0 && block_table == nullptr) || (c->num_pages > 0 && cache == nullptr))
+    return SPARGE_EINVAL;
+  if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(o, 16) || !aligned(ws, 256) ||
+      !aligned(block_table, 4) || !aligned(seq_len, 4) || !aligned(cu_q, 4) || !aligned(lse, 4))
+    return SPARGE_EINVAL;
+  if (ws_bytes < kv4_attn_ws_bytes(*c, *a)) return SPARGE_EWORKSPACE;
+  // o, lse and ws are written: they meet nothing else
+  const int64_t rows = int64_t(a->T) * a->Hq;
+  const void* p[] = {o, lse, ws, q, cache, block_table, seq_len, cu_q};
+  const int64_t n[] = {rows * c->d * 2, lse != nullptr ? rows * 4 : 0,
+                       int64_t(kv4_attn_ws_bytes(*c, *a)),
+                       ((a->T - 1) * a->q_stride + int64_t(a->Hq) * c->d) * 2,
+                       int64_t(sparge_kv4_bytes(c)), 4 * int64_t(a->R) * a->max_pages,
+                       4 * int64_t(a->R), 4 * int64_t(a->R) + 4};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 8; ++j)
+      if (n[i] > 0 && n[j] > 0 && overlap(p[i], n[i], p[j], n[j])) return SPARGE_EINVAL;
+  DeviceScope dev;
+  if ((st = dev.enter(q)) != SPARGE_OK) return st;
+  return from_cuda(launch_kv4_attn(*c, *a, q, cache, block_table, seq_len, cu_q, o, lse, ws, stream));
 }
 
 }  // extern "C"

@@ -169,6 +169,18 @@ cudaError_t launch_kv4_cache(const sparge_kv4_t& c, bool read, int32_t T, void* 
                              sparge_dtype_t dtype, const int32_t* slots, void* cache,
                              int32_t* status, cudaStream_t s);
 
+// ------------------------------------------------------------- kv4_attn.cu
+// Longest request the call may meet.
+inline int64_t kv4_len_cap(const sparge_kv4_t& c, const sparge_kv4_attn_t& a) {
+  const int64_t table = int64_t(a.max_pages) * c.page_size;
+  return a.max_len > 0 && a.max_len < table ? a.max_len : table;
+}
+bool kv4_attn_fits(const sparge_kv4_t& c, const sparge_kv4_attn_t& a);
+size_t kv4_attn_ws_bytes(const sparge_kv4_t& c, const sparge_kv4_attn_t& a);
+cudaError_t launch_kv4_attn(const sparge_kv4_t& c, const sparge_kv4_attn_t& a, const void* q,
+                            const void* cache, const int32_t* table, const int32_t* seq_len,
+                            const int32_t* cu_q, void* o, float* lse, void* ws, cudaStream_t s);
+
 // ------------------------------------------------------------- attn_sm100.cu
 struct AttnPtrs {
   const void* q;        // io dtype, or int8 codes with qk_int8

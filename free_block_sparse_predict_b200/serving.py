@@ -1,5 +1,6 @@
 """Binding of the entry points around the prompt pass (include/sparge.h): rotary
-positions with several axes, the bookkeeping of a paged cache, and the cache in 4 bits.
+positions with several axes, the bookkeeping of a paged cache, the cache in 4 bits and the
+attention over it.
 
 As in the package's main module, every ``sparge_*`` function has the name of the
 C entry point it wraps and only checks and marshals arguments; a call runs on the
@@ -8,16 +9,18 @@ device that owns its tensors, on that device's current stream unless one is give
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import NamedTuple, Optional
 
 import torch
 
-from ._native import (SPARGE_BF16, SPARGE_F16, SPARGE_F32, SpargeError, SpargeKv4, SpargeRope,
-                      lib)
+from ._native import (SPARGE_BF16, SPARGE_F16, SPARGE_F32, SpargeError, SpargeKv4, SpargeKv4Attn,
+                      SpargeRope, lib)
 
 __all__ = ["Rope", "rope_frequencies", "grid_positions", "sparge_rope_apply",
            "sparge_rope_inverse", "sparge_kv_plan", "SpargeKv4", "make_kv4", "kv4_cache",
-           "sparge_kv4_bytes", "sparge_kv4_append", "sparge_kv4_read"]
+           "sparge_kv4_bytes", "sparge_kv4_append", "sparge_kv4_read",
+           "sparge_kv4_workspace_bytes", "kv4_workspace", "sparge_kv4_attn"]
 
 _DT = {torch.float16: SPARGE_F16, torch.bfloat16: SPARGE_BF16, torch.float32: SPARGE_F32}
 
@@ -251,3 +254,57 @@ def sparge_kv4_read(c: SpargeKv4, cache, slot_map, k, v, stream=None) -> None:
     _check(lib().sparge_kv4_read(ctypes.byref(c), T, pc,
                                  _flat(slot_map, "slot_map", T, torch.int32, dev), pk, sk, pv, sv,
                                  _DT[first.dtype], _stream(stream, dev)))
+
+
+# ----------------------------------------------------------------------------
+# attention over the cache
+# ----------------------------------------------------------------------------
+
+def sparge_kv4_workspace_bytes(c: SpargeKv4, a: SpargeKv4Attn) -> int:
+    return int(lib().sparge_kv4_workspace_bytes(ctypes.byref(c), ctypes.byref(a)))
+
+
+def kv4_workspace(c: SpargeKv4, Hq: int, T: int, R: int, max_q: int, max_len: int,
+                  device="cuda") -> torch.Tensor:
+    """Workspace of sparge_kv4_attn for R requests of up to max_len tokens, T rows of q in all
+    and up to max_q each: for a block table of ceil(max_len / page_size) columns, or with that
+    max_len given to the call."""
+    pages = -(-max_len // c.page_size) if c.page_size > 0 else 0
+    a = SpargeKv4Attn(R, T, Hq, max_q, pages, max_len, 1, 1.0, SPARGE_F16, Hq * c.d)
+    n = sparge_kv4_workspace_bytes(c, a)
+    if n == 0:
+        raise _bad("invalid parameters")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def sparge_kv4_attn(c: SpargeKv4, q, cache, block_table, seq_len, cu_q, max_q: int, o, ws,
+                    scale: Optional[float] = None, causal: bool = True, lse=None,
+                    max_len: int = 0, stream=None) -> None:
+    """Attention of new tokens over the cache that holds them already.
+
+    q [T, Hq, d] (any token stride), o [T, Hq, d], lse float32 [T, Hq] or None; block_table
+    [R, max_pages], seq_len [R] and cu_q [R + 1] as sparge_kv_plan leaves them; max_q: most new
+    tokens of a request; max_len: longest request (0: what the table holds); scale: 1/sqrt(d)
+    unless given."""
+    dev = _device(q, "q")
+    if q.dim() != 3 or q.dtype not in (torch.float16, torch.bfloat16) or q.shape[2] != c.d:
+        raise _bad(f"q: expected [T, Hq, {c.d}] in 16 bits")
+    T, Hq, d = q.shape
+    sq = q.stride()
+    if sq[2] != 1 or (Hq > 1 and sq[1] != d):
+        raise _bad("q: heads and channels have to be contiguous")
+    if o.shape != q.shape:
+        raise _bad(f"o: expected {list(q.shape)}")
+    if block_table.dim() != 2:
+        raise _bad("block_table: expected [R, max_pages]")
+    (R, width), i32 = block_table.shape, torch.int32
+    if cache.device != dev or ws.device != dev or not ws.is_contiguous():
+        raise _bad(f"cache, ws: expected contiguous tensors on {dev}")
+    a = SpargeKv4Attn(R, T, Hq, max_q, width, max_len, int(causal),
+                      1.0 / math.sqrt(d) if scale is None else scale, _DT[q.dtype], sq[0])
+    _check(lib().sparge_kv4_attn(
+        ctypes.byref(c), ctypes.byref(a), q.data_ptr(), _cache_ptr(c, cache),
+        _flat(block_table, "block_table", 0, i32, dev), _flat(seq_len, "seq_len", R, i32, dev),
+        _flat(cu_q, "cu_q", R + 1, i32, dev), _flat(o, "o", 0, q.dtype, dev),
+        None if lse is None else _flat(lse, "lse", T * Hq, torch.float32, dev), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _stream(stream, dev)))

@@ -330,6 +330,41 @@ sparge_status_t sparge_kv4_read(const sparge_kv4_t* c, int32_t T, const void* ca
                                 void* v, const int64_t v_stride[2], sparge_dtype_t dtype,
                                 cudaStream_t stream);
 
+/* Attention of new tokens over the cache. */
+typedef struct {
+  int32_t R;              /* requests                                                      */
+  int32_t T;              /* rows of q and o                                               */
+  int32_t Hq;             /* query heads; head h reads KV head h / (Hq / Hkv)              */
+  int32_t max_q;          /* no request has more new tokens than this                      */
+  int32_t max_pages;      /* width of the block table                                      */
+  int32_t max_len;        /* no request is longer; 0: max_pages * page_size                */
+  int32_t causal;         /* 1: a token sees the keys up to its own; 0: all of its request */
+  float scale;            /* score scale, normally 1/sqrt(d)                               */
+  sparge_dtype_t dtype;   /* of q and o: SPARGE_F16 or SPARGE_BF16                         */
+  int64_t q_stride;       /* elements between tokens of q, heads are d apart               */
+} sparge_kv4_attn_t;
+
+/* Bytes of workspace for these parameters; 0 when they are invalid. */
+size_t sparge_kv4_workspace_bytes(const sparge_kv4_t* c, const sparge_kv4_attn_t* a);
+
+/* o[t, h, :] = sum_n softmax_n(scale q[t, h] . k_n) v_n over the keys that token t sees.
+ * Rows cu_q[r] .. cu_q[r + 1] - 1 of q and o are request r's newest tokens, the last of them
+ * at position seq_len[r] - 1 (they are in the cache already).  A row that sees no key gives
+ * 0 and lse -infinity; rows that belong to no request are left as they were.
+ *   cache, block_table [R, max_pages], seq_len [R], cu_q [R + 1]: device, as sparge_kv_plan
+ *     leaves them
+ *   o    [T, Hq, d] of dtype; lse: nullable float32 [T, Hq], log of the sum of exponentials
+ * Q is taken to fp16 with one power of two per row, products accumulate in float32, softmax
+ * statistics are float32, and weight times V's scale is rounded to fp16 once.
+ * Keys at pages outside [0, num_pages) or behind max_len are left out; these, a length below
+ * 0 and a cu_q that does not ascend within [0, T] by steps of at most max_q (such a request
+ * is skipped) put SPARGE_EINVAL into the workspace's status word (sparge_device_status).
+ * SPARGE_EUNSUPPORTED: R or Hkv > 65535, or more than 2^31 - 1 rows of q times heads. */
+sparge_status_t sparge_kv4_attn(const sparge_kv4_t* c, const sparge_kv4_attn_t* a,
+                                const void* q, const void* cache, const int32_t* block_table,
+                                const int32_t* seq_len, const int32_t* cu_q, void* o,
+                                float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* Synchronises the stream and returns the status word that kernels write to
  * the workspace (SPARGE_OK, SPARGE_ETIMEOUT or SPARGE_ERANGE), then clears it.
  * ws: the workspace of sparge_predict_mask / sparge_attn_fwd. */

@@ -153,3 +153,129 @@ def kv4_write(cache, slot, page_size, kc, ks, vc, vs):
                     b[8 * d + ((w * 8 + g) * 16 + p) * 4 + i] = (vc[h, at] + 8) | (vc[h, at + 1] + 8) << 4
         sc = np.concatenate([ks[h], vs[h]]).astype(np.float16).view(np.uint8)
         b[16 * d + k * ng * 4:16 * d + (k + 1) * ng * 4] = sc
+
+
+# ----------------------------------------------------------------------------
+# attention over the cache
+# ----------------------------------------------------------------------------
+
+class AttnCase:
+    """A filled cache, its tables and queries on the device, and the exact answer.
+
+    lens: tokens of each request (its new ones included); news: new tokens.  The cache is
+    written by the library's append; what it then holds is read back once in float32 and is
+    what the definition works on, in float64."""
+
+    def __init__(self, fb, device, lens, news, Hq, Hkv, d, group, page, dtype, seed=0, q_scale=2.0,
+                 stale=True, kscale=1.0, vscale=1.0, pad=0):
+        g = torch.Generator(device=device).manual_seed(seed)
+        self.fb, self.lens, self.news, self.pad = fb, list(lens), list(news), pad
+        R, P = len(lens), page
+        counts = [-(-max(n, 0) // P) for n in lens]
+        pages = sum(counts) + 2
+        self.c = fb.make_kv4(Hkv, d, group, P, pages)
+        self.cache = fb.kv4_cache(self.c, device)
+        # unwritten memory: any bytes, among them scales that are NaN or infinite
+        self.cache.copy_(torch.randint(0, 256, self.cache.shape, dtype=torch.uint8, device=device)
+                         if stale else torch.full_like(self.cache, 255))
+        ids = torch.randperm(pages, generator=g, device=device).int()
+        self.table = torch.full((R, max([1] + counts)), -1, dtype=torch.int32, device=device)
+        at = 0
+        for r, n in enumerate(counts):
+            self.table[r, :n] = ids[at:at + n]
+            at += n
+        self.slots = []
+        for r, n in enumerate(lens):
+            i = torch.arange(max(n, 0), device=device)
+            self.slots.append((self.table[r, i // P] * P + i % P).int())
+        flat = torch.cat(self.slots) if self.slots else torch.zeros(0, dtype=torch.int32, device=device)
+        rnd = lambda *s: torch.randn(*s, generator=g, device=device)
+        n = flat.numel()
+        k = (kscale * (rnd(n, Hkv, d) * (0.3 + torch.rand(d, generator=g, device=device)) + 0.3 * rnd(d))).to(dtype)
+        v = (vscale * rnd(n, Hkv, d)).to(dtype)
+        fb.sparge_kv4_append(self.c, k, v, flat, self.cache)
+        self.k, self.v = (torch.zeros(n, Hkv, d, device=device) for _ in "kv")
+        fb.sparge_kv4_read(self.c, self.cache, flat, self.k, self.v)
+        T = sum(news) + pad
+        self.q = (q_scale * rnd(T, Hq + 1, d)).to(dtype)[:, :Hq]
+        self.lens_t = torch.tensor(self.lens, dtype=torch.int32, device=device)
+        self.cu = torch.tensor(np.concatenate([[0], np.cumsum(news)]), dtype=torch.int32, device=device)
+        self.T, self.max_q, self.P = T, max([0] + list(news)), P
+
+    def run(self, causal=True, scale=None, lse=True, stream=None, ws=None, max_q=None, **kw):
+        fb, q = self.fb, self.q
+        o = torch.full(q.shape, 7.0, dtype=q.dtype, device=q.device)
+        out = torch.full(q.shape[:2], 5.0, device=q.device) if lse else None
+        max_q = self.max_q if max_q is None else max_q
+        if ws is None:
+            ws = fb.kv4_workspace(self.c, q.shape[1], self.T, len(self.lens), max_q,
+                                  kw.get("max_len") or self.table.shape[1] * self.P, q.device)
+        self.ws = ws
+        fb.sparge_kv4_attn(self.c, q, self.cache, self.table, self.lens_t, self.cu, max_q, o, ws,
+                           scale=scale, causal=causal, lse=out, stream=stream, **kw)
+        return o, out
+
+    def exact(self, causal=True, scale=None):
+        """(o, lse, size, err, keys): float64; per row sum_n p_n |v_n|, the E of its scores (see
+        check_attn) and the number of its keys."""
+        T, Hq, d = self.q.shape
+        Hkv = self.c.Hkv
+        scale = d ** -0.5 if scale is None else scale
+        o = torch.zeros(T, Hq, d, dtype=torch.float64, device=self.q.device)
+        lse = torch.full((T, Hq), -np.inf, dtype=torch.float64, device=self.q.device)
+        size, err, keys = torch.zeros_like(o), torch.zeros_like(lse), torch.zeros_like(lse)
+        at = row = 0
+        for n, m in zip(self.lens, self.news):
+            k, v = (x[at:at + n].double().repeat_interleave(Hq // Hkv, 1) for x in (self.k, self.v))
+            q = self.q[row:row + m].double()
+            s = torch.einsum("ihd,nhd->ihn", q, k) * scale
+            if causal:
+                see = torch.arange(n, device=q.device)[None] <= (n - m + torch.arange(m, device=q.device))[:, None]
+            else:
+                see = torch.ones(m, n, dtype=torch.bool, device=q.device)
+            s = s.masked_fill(~see[:, None], -np.inf)
+            lse[row:row + m] = torch.logsumexp(s, -1) if n else -np.inf
+            p = torch.exp(s - lse[row:row + m, :, None].clamp(min=-1e300)) if n else s
+            p = torch.where(see[:, None], p, torch.zeros_like(p))
+            o[row:row + m] = torch.einsum("ihn,nhd->ihd", p, v)
+            size[row:row + m] = torch.einsum("ihn,nhd->ihd", p, v.abs())
+            keys[row:row + m] = see.sum(-1)[:, None].double()
+            if n and m:
+                step = k.view(n, Hq, d // self.c.group, self.c.group).abs().amax(-1) * (16 / 7)
+                mass = q.abs().view(m, Hq, d // self.c.group, self.c.group).sum(-1)
+                big = torch.einsum("ihg,nhg->ihn", mass, step) * scale
+                err[row:row + m] = torch.where(see[:, None], big, torch.zeros_like(big)).amax(-1)
+            at, row = at + n, row + m
+        return o, lse, size, err, keys
+
+
+def check_attn(case, got, want):
+    """Tolerance.  Codes and scales enter exactly; so does Q, up to 2^-37 of a row's largest.
+    Scores: products of up to 7 s |q| in float32 accumulators, at most eight instructions a
+    group, each off by at most 2^-22 of the running size: 2^-19 E with E = scale sum_g 16 s_g
+    sum |q_g| and s_g = max|k_g| / 7; with the group sums and the exponent's own argument below
+    2^-17 E.  exp2 and the (at most some twenty) rescalings and joins, 2^-22 each: 2^-17.  So a
+    weight and the sum of weights are each off by w = 2^-17 (E + 1), relatively, and lse by as
+    much.  p s is rounded to fp16 once: 2^-11 sum p |v|, and below fp16's normal range 2^-25 a
+    key, times a code of up to 7 (the sum of weights is at least 1): 6 standard deviations of n
+    independent ones.  Sums of up to max |v| in n/64 (at most 512) steps a warp, each off by
+    2^-22 of them.  Then the output's rounding."""
+    (o, lse), (wo, wl, size, err, keys) = got, want
+    n = case.T - case.pad
+    w = 2.0 ** -17 * (err + 1)
+    vmax = float(case.v.abs().nan_to_num(0, 0, 0).max()) if case.v.numel() else 0.0
+    steps = (keys / 64).clamp(max=512) + 2
+    tol = (2.0 ** -11 + 2 * w)[..., None] * size + \
+        (6 * 7 * 2.0 ** -25 * keys.sqrt() + steps * 2.0 ** -22 * vmax)[..., None]
+    tol = tol * (1 + 2.0 ** -8) + torch.finfo(o.dtype).eps / 2 * wo.abs() + 2.0 ** -25
+    d = (o[:n].double() - wo[:n]).abs()
+    assert bool((d <= tol[:n]).all()), (float((d - tol[:n]).max()), float(d.max()))
+    if lse is not None:
+        fin = torch.isfinite(wl[:n])
+        assert torch.equal(torch.isfinite(lse[:n]), fin)
+        assert bool((lse[:n][~fin] == -np.inf).all())
+        dl = (lse[:n].double() - wl[:n])[fin].abs()
+        tl = (w + 2.0 ** -22 * wl.abs())[:n][fin]
+        assert bool((dl <= tl).all()), float((dl - tl).max())
+        assert bool((lse[n:] == 5).all())
+    assert bool((o[n:] == 7).all())

@@ -200,3 +200,49 @@ def test_cache_pointers_and_strides(native):
     assert read(k=None, v=None) == 0
     assert read(ks=S(0, 64)) == 1 and read(ks=S(128, 32)) == 1    # rows that overlap
     assert read(k=P(FAR[2].value - 128)) == 1                     # over the slots
+
+
+# ----------------------------------------------------------------------------
+# attention over the cache
+# ----------------------------------------------------------------------------
+
+def _attn(native, **kw):
+    a = dict(R=3, T=6, Hq=4, max_q=2, max_pages=9, max_len=0, causal=1, scale=0.125, dtype=1, q_stride=256)
+    a.update(kw)
+    return native.SpargeKv4Attn(*a.values())
+
+
+def _attn_call(native, c, a, ws_bytes=1 << 30, **swap):
+    p = dict(zip(("q", "cache", "table", "lens", "cu", "o", "lse", "ws"), FAR))
+    p.update(swap)
+    return native.lib().sparge_kv4_attn(ctypes.byref(c), ctypes.byref(a) if a else None, p["q"], p["cache"],
+                                        p["table"], p["lens"], p["cu"], p["o"], p["lse"], p["ws"], ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(R=-1), 1), (dict(T=-1), 1), (dict(Hq=0), 1), (dict(Hq=5), 1), (dict(max_q=-1), 1),
+    (dict(max_pages=-1), 1), (dict(max_len=-1), 1), (dict(causal=2), 1), (dict(scale=0.0), 1),
+    (dict(scale=float("inf")), 1), (dict(dtype=2), 1), (dict(q_stride=128), 1), (dict(q_stride=260), 2),
+    (dict(R=70000), 2), (dict(max_pages=1 << 27), 2), (dict(T=1 << 30), 2),
+    (dict(max_q=1 << 20), 2)])
+def test_attention_parameters_refused(native, kw, code):
+    c, a = _kv4(native), _attn(native, **kw)
+    assert native.lib().sparge_kv4_workspace_bytes(ctypes.byref(c), ctypes.byref(a)) == 0
+    assert _attn_call(native, c, a) == code
+
+
+def test_attention_pointers_and_workspace(native):
+    c, a = _kv4(native), _attn(native)
+    need = native.lib().sparge_kv4_workspace_bytes(ctypes.byref(c), ctypes.byref(a))
+    assert need >= 256
+    assert _attn_call(native, c, None) == 1
+    assert _attn_call(native, c, a, ws_bytes=need - 1) == 5
+    for n in ("q", "cache", "table", "lens", "cu", "o", "ws"):
+        assert _attn_call(native, c, a, **{n: None}) == 1, n
+        assert _attn_call(native, c, a, **{n: P(0x90000002)}) == 1, n
+    assert _attn_call(native, c, a, lse=P(0x90000002)) == 1
+    assert _attn_call(native, c, a, o=FAR[0]) == 1                # over q
+    assert _attn_call(native, c, a, lse=FAR[5]) == 1              # over o
+    assert _attn_call(native, c, a, ws=FAR[1]) == 1               # inside the cache
+    for kw in (dict(R=0), dict(T=0), dict(max_q=0)):
+        assert _attn_call(native, c, _attn(native, **kw), q=None, o=None) == 0
