@@ -175,7 +175,6 @@ inline int64_t kv4_len_cap(const sparge_kv4_t& c, const sparge_kv4_attn_t& a) {
   const int64_t table = int64_t(a.max_pages) * c.page_size;
   return a.max_len > 0 && a.max_len < table ? a.max_len : table;
 }
-bool kv4_attn_fits(const sparge_kv4_t& c, const sparge_kv4_attn_t& a);
 size_t kv4_attn_ws_bytes(const sparge_kv4_t& c, const sparge_kv4_attn_t& a);
 cudaError_t launch_kv4_attn(const sparge_kv4_t& c, const sparge_kv4_attn_t& a, const void* q,
                             const void* cache, const int32_t* table, const int32_t* seq_len,

@@ -224,7 +224,7 @@ def _attn_call(native, c, a, ws_bytes=1 << 30, **swap):
     (dict(max_pages=-1), 1), (dict(max_len=-1), 1), (dict(causal=2), 1), (dict(scale=0.0), 1),
     (dict(scale=float("inf")), 1), (dict(dtype=2), 1), (dict(q_stride=128), 1), (dict(q_stride=260), 2),
     (dict(R=70000), 2), (dict(max_pages=1 << 27), 2), (dict(T=1 << 30), 2),
-    (dict(max_q=1 << 20), 2)])
+    (dict(max_q=1 << 30), 2)])
 def test_attention_parameters_refused(native, kw, code):
     c, a = _kv4(native), _attn(native, **kw)
     assert native.lib().sparge_kv4_workspace_bytes(ctypes.byref(c), ctypes.byref(a)) == 0
