@@ -26,7 +26,8 @@
 //
 // Work is cut evenly, whatever the lengths: the units (request, KV head, tile
 // of 8 NT query rows) stand in one line, each as long as its keys in pairs of
-// 16-token tiles, and CTA c of C takes the c-th part of the line.  A unit that
+// 16-token tiles and a constant for its start and end, and CTA c of C takes the
+// c-th part of the line.  A unit that
 // lies within one CTA is finished there; the parts of a cut one go to the
 // workspace, and the CTA that arrives last joins them in the order of their
 // keys.  The cut depends on the lengths alone, so results are the same bits
@@ -150,6 +151,12 @@ __device__ __forceinline__ Request request(const DecodeArgs& A, int r) {
   return x;
 }
 
+// A unit's start and end cost a CTA about as much as this many pairs: the
+// queries, the first copies' latency, the joining (3.5 us against 0.4 us a pair
+// with every SM full).  Without it, many short requests met one CTA: nine
+// requests of 4001 to 1 tokens took 45 us, not NINE_US.
+constexpr int kUnitCost = 8;
+
 // Length of request r's units in pairs of tiles (a unit without keys still has
 // its rows to write), and how many there are.
 __device__ __forceinline__ int64_t unit_pairs(const Request& x) {
@@ -172,6 +179,7 @@ struct Cfg {
   static constexpr int SMEM = kWarps * RING;
   static constexpr int CTAS = NT == 1 ? 4 : 2;  // per SM, by registers
   static_assert(ROWS * PITCH * 4 <= RING, "a warp's result fits its ring");
+  static_assert(kSms * CTAS * ROWS * 8 <= SMEM, "so do the weights of all CTAs' parts");
   static_assert(CTAS * (SMEM + 2048) <= 228 * 1024, "resident together");
 };
 
@@ -250,12 +258,11 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
   // ---- the line of units: its length, and the request where this part starts
   const int per = (A.R + kAttnThreads - 1) / kAttnThreads;
   const int r_lo = min(A.R, int(threadIdx.x) * per), r_hi = min(A.R, r_lo + per);
-  int64_t own = 0, units = 0;
+  int64_t own = 0;
   for (int r = r_lo; r < r_hi; ++r) {
     const Request x = request(A, r);
     const int64_t n = unit_count<C::ROWS>(A, x);
-    own += n * unit_pairs(x);
-    units += n;
+    own += n * (unit_pairs(x) + kUnitCost);
     if (!x.sound && blockIdx.x == 0) atomicCAS(A.status, 0, int32_t(SPARGE_EINVAL));
   }
   int64_t incl = own;
@@ -263,31 +270,26 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += up;
-    units += __shfl_xor_sync(0xffffffffu, units, o);
   }
   if (lane == 31) s_scan[warp] = incl;
-  if (lane == 0) s_ml[warp][0].x = float(units < 100000 ? units : 100000);
   __syncthreads();
   int64_t total = 0, before = 0;
-  int all_units = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
-    all_units += int(s_ml[w][0].x);
   }
   before += incl - own;
-  // parts: a pair per warp at least, and not more than 96 to a unit on average
+  // parts: a pair per warp at least
   int64_t parts = gridDim.x;
   if (parts > (total + kWarps - 1) / kWarps) parts = (total + kWarps - 1) / kWarps;
-  if (parts > int64_t(96) * all_units) parts = int64_t(96) * all_units;
   if (int64_t(blockIdx.x) >= parts) return;
   const int64_t line0 = blockIdx.x * total / parts, line1 = (blockIdx.x + 1) * total / parts;
   if (before <= line0 && line0 < before + own) {
     int64_t at = before;
     for (int r = r_lo; r < r_hi; ++r) {
       const Request x = request(A, r);
-      const int64_t n = unit_count<C::ROWS>(A, x) * unit_pairs(x);
+      const int64_t n = unit_count<C::ROWS>(A, x) * (unit_pairs(x) + kUnitCost);
       if (line0 < at + n) {
         s_found[0] = r;
         s_found[1] = at;
@@ -305,20 +307,21 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
 
   for (int64_t line = line0; line < line1;) {
     Request req = request(A, r);
-    int64_t n_pairs = unit_pairs(req), n_units = unit_count<C::ROWS>(A, req);
-    if (line >= r_at + n_units * n_pairs) {
-      r_at += n_units * n_pairs;
+    const int64_t n_pairs = unit_pairs(req), n_units = unit_count<C::ROWS>(A, req);
+    const int64_t length = n_pairs + kUnitCost;
+    if (line >= r_at + n_units * length) {
+      r_at += n_units * length;
       ++r;
       continue;
     }
-    const int64_t unit = (line - r_at) / n_pairs;
-    const int64_t unit_at = r_at + unit * n_pairs;
-    const int pair0 = int(line - unit_at);
-    const int64_t stop = min(line1, unit_at + n_pairs);
-    const int pair1 = int(stop - unit_at);
-    const bool cut = pair0 > 0 || pair1 < n_pairs;
-    const bool first = line == line0;
+    const int64_t unit = (line - r_at) / length;
+    const int64_t pairs_at = r_at + unit * length + kUnitCost;  // where its first pair stands
+    const int pair0 = int(max(line - pairs_at, int64_t(0)));
+    const int64_t stop = min(line1, pairs_at + n_pairs);
+    const int pair1 = int(max(stop - pairs_at, int64_t(0)));
     line = stop;
+    if (pair1 == pair0) continue;  // the next CTA has all of it
+    const bool cut = pair0 > 0 || pair1 < n_pairs;
     const int kvh = int(unit % A.Hkv), row0 = int(unit / A.Hkv) * C::ROWS;
     const int rows = req.qlen * A.G;
     // the last key that any row of this tile sees
@@ -649,7 +652,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
     __syncthreads();
 
     // ---- the warps joined: finished, or this CTA's part of a cut unit
-    const int64_t slot = 2 * int64_t(blockIdx.x) + (first ? 0 : 1);
+    const int64_t slot = 2 * int64_t(blockIdx.x) + (pair0 > 0 ? 0 : 1);
     const int here_rows = min(C::ROWS, rows - row0);
     for (int e = threadIdx.x; e < here_rows * (D / 2); e += kAttnThreads) {
       const int row = e / (D / 2), ch = 2 * (e % (D / 2));
@@ -680,38 +683,82 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
     __syncthreads();
     if (!cut) continue;
 
-    // ---- the last of a cut unit's CTAs joins its parts
-    const int64_t c0 = ((unit_at + 1) * parts - 1) / total;
-    const int64_t c1 = ((unit_at + n_pairs) * parts - 1) / total;
+    // ---- the last of a cut unit's CTAs joins its parts, in their order
+    const int64_t c0 = ((pairs_at + 1) * parts - 1) / total;
+    const int n_parts = int(((pairs_at + n_pairs) * parts - 1) / total - c0) + 1;
     if (threadIdx.x == 0)
-      s_flag[1] = atomicInc(A.arrived + c0, uint32_t(c1 - c0)) == uint32_t(c1 - c0);
+      s_flag[1] = atomicInc(A.arrived + c0, uint32_t(n_parts - 1)) == uint32_t(n_parts - 1);
     __syncthreads();
     if (!s_flag[1]) continue;
     __threadfence();
-    const bool head_first = c0 * total / parts == unit_at;  // it starts CTA c0's part
-    for (int e = threadIdx.x; e < here_rows * (D / 2); e += kAttnThreads) {
-      const int row = e / (D / 2), ch = 2 * (e % (D / 2));
-      float top = kLow;
-#pragma unroll 4
-      for (int64_t c = c0; c <= c1; ++c) {
-        const int64_t sl = 2 * c + (c == c0 && !head_first ? 1 : 0);
-        top = fmaxf(top, __ldcg(A.part_ml + sl * C::ROWS + row).x);
+    // the first part is its CTA's last unit, the others are their CTAs' first
+    const int64_t row_at = (2 * c0 + 1) * C::ROWS;  // of the first; the next is at 2 (c0 + 1)
+    auto part_row = [&](int k, int row) {
+      return row_at + (k > 0 ? (2 * k - 1) * C::ROWS : 0) + row;
+    };
+    float2* s_part = reinterpret_cast<float2*>(smem);  // [part][row]: weight (maximum), sum
+    for (int e = threadIdx.x; e < n_parts * C::ROWS; e += kAttnThreads)
+      s_part[e] = __ldcg(A.part_ml + part_row(e / C::ROWS, e % C::ROWS));
+    __syncthreads();
+    // a thread per row: the rows' weights, and their sums
+    if (threadIdx.x < C::ROWS) {
+      float top = kLow, sum = 0.f;
+      for (int k = 0; k < n_parts; ++k) top = fmaxf(top, s_part[k * C::ROWS + threadIdx.x].x);
+      for (int k = 0; k < n_parts; ++k) {
+        float2& p = s_part[k * C::ROWS + threadIdx.x];
+        p.x = ex2_approx(p.x - top);
+        sum = fmaf(p.y, p.x, sum);
       }
-      float sum = 0.f, x = 0.f, y = 0.f;
-#pragma unroll 4
-      for (int64_t c = c0; c <= c1; ++c) {
-        const int64_t sl = 2 * c + (c == c0 && !head_first ? 1 : 0);
-        const float2 ml = __ldcg(A.part_ml + sl * C::ROWS + row);
-        const float2 v = __ldcg(
-            reinterpret_cast<const float2*>(A.part_o + (sl * C::ROWS + row) * D + ch));
-        const float a = ex2_approx(ml.x - top);
-        sum = fmaf(ml.y, a, sum);
-        x = fmaf(v.x, a, x);
-        y = fmaf(v.y, a, y);
+      s_ml[0][threadIdx.x] = make_float2(top, sum);
+    }
+    __syncthreads();
+    // every warp takes each fourth part, all rows of it at once
+    constexpr int V = 4;                   // channels per lane
+    constexpr int RPW = 32 * V / D;        // rows a warp's load covers
+    constexpr int ITEMS = C::ROWS / RPW;
+    const int ch = V * lane % D, sub = V * lane / D;
+    float x[ITEMS][V];
+#pragma unroll
+    for (int e = 0; e < ITEMS; ++e)
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[e][v] = 0.f;
+#pragma unroll 2
+    for (int k = warp; k < n_parts; k += kWarps) {
+#pragma unroll
+      for (int e = 0; e < ITEMS; ++e) {
+        const int row = e * RPW + sub;
+        if (row < here_rows) {
+          const float4 q = __ldcg(reinterpret_cast<const float4*>(A.part_o + part_row(k, row) * D + ch));
+          const float a = s_part[k * C::ROWS + row].x;
+          x[e][0] = fmaf(q.x, a, x[e][0]);
+          x[e][1] = fmaf(q.y, a, x[e][1]);
+          x[e][2] = fmaf(q.z, a, x[e][2]);
+          x[e][3] = fmaf(q.w, a, x[e][3]);
+        }
+      }
+    }
+    __syncthreads();  // the weights have been read
+    float* mine_o = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int e = 0; e < ITEMS; ++e)
+      *reinterpret_cast<float4*>(mine_o + (e * RPW + sub) * D + ch) =
+          make_float4(x[e][0], x[e][1], x[e][2], x[e][3]);
+    __syncthreads();
+    for (int e = threadIdx.x; e < here_rows * (D / 2); e += kAttnThreads) {
+      const int row = e / (D / 2), c2 = 2 * (e % (D / 2));
+      float y0 = 0.f, y1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 v = *reinterpret_cast<const float2*>(
+            reinterpret_cast<const float*>(smem + w * C::RING) + row * D + c2);
+        y0 += v.x;
+        y1 += v.y;
       }
       const int q = (row0 + row) / A.G, head = kvh * A.G + (row0 + row) % A.G;
-      write_out(A, int64_t(req.q0 + q) * A.Hq + head, D, ch, top, sum, x, y);
+      write_out(A, int64_t(req.q0 + q) * A.Hq + head, D, c2, s_ml[0][row].x, s_ml[0][row].y, y0, y1);
     }
+    fence_async_shared();
+    __syncthreads();
   }
 }
 
@@ -736,7 +783,9 @@ Plan make_plan(const sparge_kv4_t& c, const sparge_kv4_attn_t& a) {
   return p;
 }
 
-size_t arrived_bytes(const Plan& p) { return align256(size_t(p.grid) * 4); }
+// Of one size for every call, so that calls of different shapes may share a
+// workspace: no other region ever lies on the counters.
+size_t arrived_bytes(const Plan&) { return align256(size_t(kSms) * 4 * sizeof(uint32_t)); }
 size_t ml_bytes(const Plan& p) { return align256(size_t(p.grid) * 2 * 8 * p.nt * sizeof(float2)); }
 
 template <int D, int NG, int NT>

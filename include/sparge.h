@@ -344,7 +344,10 @@ typedef struct {
   int64_t q_stride;       /* elements between tokens of q, heads are d apart               */
 } sparge_kv4_attn_t;
 
-/* Bytes of workspace for these parameters; 0 when they are invalid. */
+/* Bytes of workspace for these parameters; 0 when they are invalid.  It must be zeroed once,
+ * before its first use (and again after a device status of SPARGE_ETIMEOUT); calls of
+ * different shapes may share one, if it is large enough for each and they do not overlap in
+ * time. */
 size_t sparge_kv4_workspace_bytes(const sparge_kv4_t* c, const sparge_kv4_attn_t* a);
 
 /* o[t, h, :] = sum_n softmax_n(scale q[t, h] . k_n) v_n over the keys that token t sees.

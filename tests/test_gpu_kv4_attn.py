@@ -188,6 +188,16 @@ def test_captured_call_follows_its_buffers():
     assert fb.sparge_device_status(ws) == 0
 
 
+def test_calls_of_different_shapes_share_a_workspace():
+    """Large and small, one row tile and many: each leaves the workspace fit for the next."""
+    cases = [AttnCase(fb, dev(), lens, news, 8, 2, 128, 32, 32, torch.bfloat16, seed=i) for i, (lens, news) in
+             enumerate([([9000, 70], [1, 1]), ([70, 33, 40], [70, 33, 40]), ([5], [1]), ([2000] * 30, [1] * 30)])]
+    need = [case.run() and case.ws.numel() for case in cases]
+    ws = torch.zeros(max(need), dtype=torch.uint8, device=dev())
+    for i in (0, 1, 2, 1, 0, 3, 2, 1, 3, 0):
+        check(cases[i], ws=ws)
+
+
 def test_cache_past_32_bits():
     """Pages that lie beyond 2^32 bytes."""
     c = fb.make_kv4(1, 128, 32, 1024, 1 << 15)
