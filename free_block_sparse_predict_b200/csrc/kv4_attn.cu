@@ -53,6 +53,26 @@ constexpr int kAttnThreads = kWarps * 32;
 constexpr float kLow = -1e30f;     // "no key yet"; finite, so differences stay numbers
 constexpr float kLazy = 2.0f;      // log2 units
 
+// Division by a number that the host knows: n / d = umulhi(n, mul) >> shift
+// for n < 2^31 (Granlund and Montgomery's round-up method, 32 + 1 bits of
+// precision for a 31-bit numerator).
+struct Div {
+  uint32_t d, mul, shift;
+  __device__ __forceinline__ int32_t quot(int32_t n) const {
+    return d == 1 ? n : int32_t(__umulhi(uint32_t(n), mul) >> shift);
+  }
+};
+Div make_div(uint32_t d) {
+  Div x{d, 0, 0};
+  if (d > 1) {
+    uint32_t log = 0;
+    while ((uint64_t(1) << log) < d) ++log;  // ceil(log2 d)
+    x.shift = log - 1;
+    x.mul = uint32_t(((uint64_t(1) << (31 + log)) + d - 1) / d);
+  }
+  return x;
+}
+
 struct Masks {
   uint32_t low, high;  // 0x000F000F, 0x00F000F0
 };
@@ -69,7 +89,8 @@ struct DecodeArgs {
   uint32_t* arrived;  // [C]: parts of the unit that starts in CTA c; 0 between calls
   int32_t* status;
   int64_t q_stride;  // bytes
-  int32_t R, T, Hq, Hkv, G, max_q, max_pages, len_cap, causal, tpp, num_pages, bf16;
+  int32_t R, T, Hq, Hkv, max_q, max_pages, len_cap, causal, num_pages, bf16;
+  Div G, heads, tpp;  // query heads per KV head, KV heads, tiles per page
   Masks masks;
   float scale_log2;
 };
@@ -164,7 +185,7 @@ __device__ __forceinline__ int64_t unit_pairs(const Request& x) {
 }
 template <int ROWS>
 __device__ __forceinline__ int64_t unit_count(const DecodeArgs& A, const Request& x) {
-  return int64_t(A.Hkv) * ((int64_t(x.qlen) * A.G + ROWS - 1) / ROWS);
+  return int64_t(A.Hkv) * ((int64_t(x.qlen) * A.G.d + ROWS - 1) / ROWS);
 }
 
 template <int D, int NG, int NT>
@@ -179,7 +200,6 @@ struct Cfg {
   static constexpr int SMEM = kWarps * RING;
   static constexpr int CTAS = NT == 1 ? 4 : 2;  // per SM, by registers
   static_assert(ROWS * PITCH * 4 <= RING, "a warp's result fits its ring");
-  static_assert(kSms * CTAS * ROWS * 8 <= SMEM, "so do the weights of all CTAs' parts");
   static_assert(CTAS * (SMEM + 2048) <= 228 * 1024, "resident together");
 };
 
@@ -207,6 +227,12 @@ __device__ __forceinline__ void load_scales(const uint8_t* at, float (&k)[NG], f
       v[2 * i] = y.x, v[2 * i + 1] = y.y;
     }
   }
+}
+
+// Row `row` (query token times head of the group) of a request and KV head in q and o.
+__device__ __forceinline__ int64_t out_row(const DecodeArgs& A, const Request& x, int kvh, int row) {
+  const int tok = A.G.quot(row);
+  return int64_t(x.q0 + tok) * A.Hq + kvh * int(A.G.d) + (row - tok * int(A.G.d));
 }
 
 // One row's final value pair and, from the thread of its first channel, lse.
@@ -283,8 +309,10 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
   // parts: a pair per warp at least
   int64_t parts = gridDim.x;
   if (parts > (total + kWarps - 1) / kWarps) parts = (total + kWarps - 1) / kWarps;
-  if (int64_t(blockIdx.x) >= parts) return;
-  const int64_t line0 = blockIdx.x * total / parts, line1 = (blockIdx.x + 1) * total / parts;
+  if (total == 0) return;
+  const int64_t step = (total + parts - 1) / parts;
+  const int64_t line0 = blockIdx.x * step, line1 = min(line0 + step, total);
+  if (line0 >= total) return;
   if (before <= line0 && line0 < before + own) {
     int64_t at = before;
     for (int r = r_lo; r < r_hi; ++r) {
@@ -314,7 +342,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
       ++r;
       continue;
     }
-    const int64_t unit = (line - r_at) / length;
+    const int64_t into = line - r_at;
+    const int64_t unit = (into | length) >> 32 ? into / length : uint32_t(into) / uint32_t(length);
     const int64_t pairs_at = r_at + unit * length + kUnitCost;  // where its first pair stands
     const int pair0 = int(max(line - pairs_at, int64_t(0)));
     const int64_t stop = min(line1, pairs_at + n_pairs);
@@ -322,12 +351,12 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
     line = stop;
     if (pair1 == pair0) continue;  // the next CTA has all of it
     const bool cut = pair0 > 0 || pair1 < n_pairs;
-    const int kvh = int(unit % A.Hkv), row0 = int(unit / A.Hkv) * C::ROWS;
-    const int rows = req.qlen * A.G;
+    const int tile_of = A.heads.quot(int(unit)), kvh = int(unit) - tile_of * A.Hkv;
+    const int row0 = tile_of * C::ROWS, rows = req.qlen * int(A.G.d);
     // the last key that any row of this tile sees
     const int last_row = min(row0 + C::ROWS, rows) - 1;
     const int32_t reach =
-        A.causal ? min(req.keys, req.len - req.qlen + last_row / A.G + 1) : req.keys;
+        A.causal ? min(req.keys, req.len - req.qlen + A.G.quot(last_row) + 1) : req.keys;
     const int n_tiles = reach > 0 ? (reach + 15) / 16 : 0;
     const int n_here = min(pair1, (n_tiles + 1) / 2) - pair0;
     // pair i of this warp is pair pair0 + warp + kWarps i of the unit
@@ -340,12 +369,12 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
       const int i = 16 * batch + (lane >> 1);
       const int ti = 2 * (pair0 + warp + kWarps * i) + (lane & 1);
       if (i >= mine || ti >= n_tiles) return -1;
-      const int32_t page = __ldg(table + ti / A.tpp);
+      const int32_t entry = A.tpp.quot(ti), page = __ldg(table + entry);
       if (uint32_t(page) >= uint32_t(A.num_pages)) {
         atomicCAS(A.status, 0, int32_t(SPARGE_EINVAL));
         return -1;
       }
-      return (page * A.Hkv + kvh) * A.tpp + ti % A.tpp;
+      return (page * A.Hkv + kvh - entry) * int32_t(A.tpp.d) + ti;
     };
     int32_t* ids = reinterpret_cast<int32_t*>(s_id[warp]);
     ids[lane] = tile_id(0);
@@ -392,7 +421,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
     for (int nt = 0; nt < NT; ++nt) {
       const int row = row0 + 8 * nt + g;
       const bool there = row < rows;
-      const int tok = there ? row / A.G : 0, head = kvh * A.G + (there ? row % A.G : 0);
+      const int tok = there ? A.G.quot(row) : 0;
+      const int head = kvh * int(A.G.d) + (there ? row - tok * int(A.G.d) : 0);
       const char* src = A.q + int64_t(req.q0 + tok) * A.q_stride + int64_t(head) * (D * 2);
       float x[J][8];
       float big = 0.f;
@@ -416,29 +446,32 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
       }
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-      // the row's largest goes to [2^12, 2^13): two factors, since one may overflow
-      int k = 0;
-      if (big > 0.f && big < INFINITY) k = 12 - ilogbf(big);
-      const float k1 = ldexpf(1.f, k / 2), k2 = ldexpf(1.f, k - k / 2);
+      // the row's largest goes to [2^12, 2^13) (a subnormal below); two factors,
+      // since one may overflow
+      const int field = int(__float_as_uint(big) >> 23);
+      const int k = field < 255 ? 139 - field : 0, half_k = k >> 1;
+      const auto two_to = [](int n) { return __uint_as_float(uint32_t(n + 127) << 23); };
+      const float k1 = two_to(half_k), k2 = two_to(k - half_k);
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           qf[nt][2 * j + i / 2][i & 1] =
               pack_half2(x[j][2 * i] * k1 * k2, x[j][2 * i + 1] * k1 * k2);
-      const float fr = A.scale_log2 * ldexpf(1.f, -k);
+      const float fr = A.scale_log2 * two_to(-half_k) * two_to(half_k - k);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         f[nt][c] = __shfl_sync(0xffffffffu, fr, (2 * t + c) * 4);  // from a lane of column 2t + c
         const int row_c = row0 + 8 * nt + 2 * t + c;
         lim[nt][c] = 0;
         if (row_c < rows)
-          lim[nt][c] = A.causal ? min(req.keys, req.len - req.qlen + row_c / A.G + 1) : req.keys;
+          lim[nt][c] =
+              A.causal ? min(req.keys, req.len - req.qlen + A.G.quot(row_c) + 1) : req.keys;
       }
     }
     // keys below this are seen by every row that is there
     int32_t all_see = req.keys;
-    if (A.causal) all_see = min(all_see, req.len - req.qlen + row0 / A.G + 1);
+    if (A.causal) all_see = min(all_see, req.len - req.qlen + A.G.quot(row0) + 1);
 
     float m[NT][2], l[NT][2];
     float o[NT][MT][4];
@@ -654,109 +687,106 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
     // ---- the warps joined: finished, or this CTA's part of a cut unit
     const int64_t slot = 2 * int64_t(blockIdx.x) + (pair0 > 0 ? 0 : 1);
     const int here_rows = min(C::ROWS, rows - row0);
-    for (int e = threadIdx.x; e < here_rows * (D / 2); e += kAttnThreads) {
-      const int row = e / (D / 2), ch = 2 * (e % (D / 2));
-      float top = kLow;
+    auto join_warps = [&](bool finish) {
+      for (int e = threadIdx.x; e < here_rows * (D / 2); e += kAttnThreads) {
+        const int row = e / (D / 2), ch = 2 * (e % (D / 2));
+        float top = kLow;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][row].x);
-      float sum = 0.f, x = 0.f, y = 0.f;
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w][row].x);
+        float sum = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 ml = s_ml[w][row];
-        const float a = ex2_approx(ml.x - top);
-        const float2 v = *reinterpret_cast<const float2*>(
-            reinterpret_cast<const float*>(smem + w * C::RING) + row * C::PITCH + ch);
-        sum = fmaf(ml.y, a, sum);
-        x = fmaf(v.x, a, x);
-        y = fmaf(v.y, a, y);
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 ml = s_ml[w][row];
+          const float a = ex2_approx(ml.x - top);
+          const float2 v = *reinterpret_cast<const float2*>(
+              reinterpret_cast<const float*>(smem + w * C::RING) + row * C::PITCH + ch);
+          sum = fmaf(ml.y, a, sum);
+          x = fmaf(v.x, a, x);
+          y = fmaf(v.y, a, y);
+        }
+        if (finish) {
+          write_out(A, out_row(A, req, kvh, row0 + row), D, ch, top, sum, x, y);
+        } else {
+          *reinterpret_cast<float2*>(A.part_o + (slot * C::ROWS + row) * D + ch) =
+              make_float2(x, y);
+          if (ch == 0) A.part_ml[slot * C::ROWS + row] = make_float2(top, sum);
+        }
       }
-      if (cut) {
-        *reinterpret_cast<float2*>(A.part_o + (slot * C::ROWS + row) * D + ch) = make_float2(x, y);
-        if (ch == 0) A.part_ml[slot * C::ROWS + row] = make_float2(top, sum);
-      } else {
-        const int q = (row0 + row) / A.G, head = kvh * A.G + (row0 + row) % A.G;
-        write_out(A, int64_t(req.q0 + q) * A.Hq + head, D, ch, top, sum, x, y);
-      }
-    }
+    };
+    join_warps(!cut);
     fence_async_shared();  // before the ring's next bulk copies
     if (cut) __threadfence();
     __syncthreads();
     if (!cut) continue;
 
-    // ---- the last of a cut unit's CTAs joins its parts, in their order
-    const int64_t c0 = ((pairs_at + 1) * parts - 1) / total;
-    const int n_parts = int(((pairs_at + n_pairs) * parts - 1) / total - c0) + 1;
+    // ---- the last of a cut unit's CTAs joins its parts: a warp each fourth of
+    // them, in their order, then the warps as above
+    const int64_t c0 = pair0 == 0 ? blockIdx.x : pairs_at / step;
+    const int n_parts = int((pairs_at + n_pairs - 1) / step - c0) + 1;
     if (threadIdx.x == 0)
       s_flag[1] = atomicInc(A.arrived + c0, uint32_t(n_parts - 1)) == uint32_t(n_parts - 1);
     __syncthreads();
     if (!s_flag[1]) continue;
     __threadfence();
-    // the first part is its CTA's last unit, the others are their CTAs' first
-    const int64_t row_at = (2 * c0 + 1) * C::ROWS;  // of the first; the next is at 2 (c0 + 1)
-    auto part_row = [&](int k, int row) {
-      return row_at + (k > 0 ? (2 * k - 1) * C::ROWS : 0) + row;
-    };
-    float2* s_part = reinterpret_cast<float2*>(smem);  // [part][row]: weight (maximum), sum
-    for (int e = threadIdx.x; e < n_parts * C::ROWS; e += kAttnThreads)
-      s_part[e] = __ldcg(A.part_ml + part_row(e / C::ROWS, e % C::ROWS));
-    __syncthreads();
-    // a thread per row: the rows' weights, and their sums
-    if (threadIdx.x < C::ROWS) {
-      float top = kLow, sum = 0.f;
-      for (int k = 0; k < n_parts; ++k) top = fmaxf(top, s_part[k * C::ROWS + threadIdx.x].x);
-      for (int k = 0; k < n_parts; ++k) {
-        float2& p = s_part[k * C::ROWS + threadIdx.x];
-        p.x = ex2_approx(p.x - top);
-        sum = fmaf(p.y, p.x, sum);
-      }
-      s_ml[0][threadIdx.x] = make_float2(top, sum);
-    }
-    __syncthreads();
-    // every warp takes each fourth part, all rows of it at once
     constexpr int V = 4;                   // channels per lane
-    constexpr int RPW = 32 * V / D;        // rows a warp's load covers
+    constexpr int RPW = 32 * V / D;        // rows that a warp's load covers
     constexpr int ITEMS = C::ROWS / RPW;
+    constexpr int BATCH = NT == 1 ? 4 : 2;  // parts in flight
     const int ch = V * lane % D, sub = V * lane / D;
-    float x[ITEMS][V];
+    float top[ITEMS], sum[ITEMS], x[ITEMS][V];
 #pragma unroll
-    for (int e = 0; e < ITEMS; ++e)
+    for (int e = 0; e < ITEMS; ++e) {
+      top[e] = kLow, sum[e] = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) x[e][v] = 0.f;
-#pragma unroll 2
-    for (int k = warp; k < n_parts; k += kWarps) {
+    }
+    for (int k0 = warp; k0 < n_parts; k0 += kWarps * BATCH) {
 #pragma unroll
       for (int e = 0; e < ITEMS; ++e) {
         const int row = e * RPW + sub;
-        if (row < here_rows) {
-          const float4 q = __ldcg(reinterpret_cast<const float4*>(A.part_o + part_row(k, row) * D + ch));
-          const float a = s_part[k * C::ROWS + row].x;
-          x[e][0] = fmaf(q.x, a, x[e][0]);
-          x[e][1] = fmaf(q.y, a, x[e][1]);
-          x[e][2] = fmaf(q.z, a, x[e][2]);
-          x[e][3] = fmaf(q.w, a, x[e][3]);
+        if (e * RPW >= here_rows) break;
+        float2 ml[BATCH];
+        float4 q[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const int k = k0 + kWarps * i;
+          ml[i] = make_float2(kLow, 0.f);
+          q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k < n_parts && row < here_rows) {
+            // the first part is its CTA's last unit, the others are their CTAs' first
+            const int64_t at = (2 * (c0 + k) + (k == 0 ? 1 : 0)) * C::ROWS + row;
+            ml[i] = __ldcg(A.part_ml + at);
+            q[i] = __ldcg(reinterpret_cast<const float4*>(A.part_o + at * D + ch));
+          }
+        }
+        float now = top[e];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) now = fmaxf(now, ml[i].x);
+        const float old = ex2_approx(top[e] - now);
+        top[e] = now;
+        sum[e] *= old;
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[e][v] *= old;
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+          const float a = ex2_approx(ml[i].x - now);
+          sum[e] = fmaf(ml[i].y, a, sum[e]);
+          x[e][0] = fmaf(q[i].x, a, x[e][0]);
+          x[e][1] = fmaf(q[i].y, a, x[e][1]);
+          x[e][2] = fmaf(q[i].z, a, x[e][2]);
+          x[e][3] = fmaf(q[i].w, a, x[e][3]);
         }
       }
     }
-    __syncthreads();  // the weights have been read
-    float* mine_o = reinterpret_cast<float*>(ring);
 #pragma unroll
-    for (int e = 0; e < ITEMS; ++e)
-      *reinterpret_cast<float4*>(mine_o + (e * RPW + sub) * D + ch) =
+    for (int e = 0; e < ITEMS; ++e) {
+      const int row = e * RPW + sub;
+      *reinterpret_cast<float4*>(so + row * C::PITCH + ch) =
           make_float4(x[e][0], x[e][1], x[e][2], x[e][3]);
-    __syncthreads();
-    for (int e = threadIdx.x; e < here_rows * (D / 2); e += kAttnThreads) {
-      const int row = e / (D / 2), c2 = 2 * (e % (D / 2));
-      float y0 = 0.f, y1 = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(
-            reinterpret_cast<const float*>(smem + w * C::RING) + row * D + c2);
-        y0 += v.x;
-        y1 += v.y;
-      }
-      const int q = (row0 + row) / A.G, head = kvh * A.G + (row0 + row) % A.G;
-      write_out(A, int64_t(req.q0 + q) * A.Hq + head, D, c2, s_ml[0][row].x, s_ml[0][row].y, y0, y1);
+      if (ch == 0) s_ml[warp][row] = make_float2(top[e], sum[e]);
     }
+    __syncthreads();
+    join_warps(true);
     fence_async_shared();
     __syncthreads();
   }
@@ -833,12 +863,13 @@ cudaError_t launch_kv4_attn(const sparge_kv4_t& c, const sparge_kv4_attn_t& a, c
   d.T = a.T;
   d.Hq = a.Hq;
   d.Hkv = c.Hkv;
-  d.G = a.Hq / c.Hkv;
+  d.G = make_div(uint32_t(a.Hq / c.Hkv));
+  d.heads = make_div(uint32_t(c.Hkv));
+  d.tpp = make_div(uint32_t(c.page_size / 16));
   d.max_q = a.max_q;
   d.max_pages = a.max_pages;
   d.len_cap = int32_t(kv4_len_cap(c, a));
   d.causal = a.causal;
-  d.tpp = c.page_size / 16;
   d.num_pages = c.num_pages;
   d.bf16 = a.dtype == SPARGE_BF16;
   d.masks = Masks{0x000F000Fu, 0x00F000F0u};
