@@ -25,13 +25,13 @@
 // p s below 65504.
 //
 // Work is cut evenly, whatever the lengths: the units (request, KV head, tile
-// of 8 NT query rows) stand in one line, each as long as its keys in pairs of
-// 16-token tiles and a constant for its start and end, and CTA c of C takes the
+// of 8 NT query rows) stand in one line, each as long as its keys in steps of
+// four (or two) 16-token tiles and a constant for its start and end, and CTA c of C takes the
 // c-th part of the line.  A unit that
 // lies within one CTA is finished there; the parts of a cut one go to the
 // workspace, and the CTA that arrives last joins them in the order of their
 // keys.  The cut depends on the lengths alone, so results are the same bits
-// every time.  Inside a CTA the four warps take the pairs in turn, each through
+// every time.  Inside a CTA the four warps take the steps in turn, each through
 // a ring of bulk copies of its own, and are joined in shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -111,15 +111,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The first of a sum.
-__device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                              uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%10,%10,%10,%10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -144,6 +135,12 @@ __device__ __forceinline__ uint32_t codes0(uint32_t w, const Masks& k) {
 }
 __device__ __forceinline__ uint32_t codes4(uint32_t w, const Masks& k) {
   return minus(pick(w, k.high, 0x54005400u), 0x54805480u);  // 64 + u, 72
+}
+// The same with the 72 left on: K's sums start at -72 times the sum of those
+// channels of Q instead (exact numbers of 4.5 times the codes' size: their
+// float32 sums lose two bits more, which 2^-22 allows).
+__device__ __forceinline__ uint32_t raised4(uint32_t w, const Masks& k) {
+  return pick(w, k.high, 0x54005400u);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -172,60 +169,60 @@ __device__ __forceinline__ Request request(const DecodeArgs& A, int r) {
   return x;
 }
 
-// A unit's start and end cost a CTA about as much as this many pairs: the
-// queries, the first copies' latency, the joining (3.5 us against 0.4 us a pair
-// with every SM full).  Without it, many short requests met one CTA: nine
-// requests of 4001 to 1 tokens took 45 us, not NINE_US.
-constexpr int kUnitCost = 8;
+// A unit's start and end cost a CTA about as much as this many keys: the
+// queries, the first copies' latency, the joining (3.5 us against 0.4 us for 32
+// keys with every SM full).  Without it, many short requests met one CTA: nine
+// requests of 4001 to 1 tokens took 45 us, with it 15.
+constexpr int kUnitKeys = 256;
 
-// Length of request r's units in pairs of tiles (a unit without keys still has
-// its rows to write), and how many there are.
-__device__ __forceinline__ int64_t unit_pairs(const Request& x) {
-  return x.keys > 0 ? (int64_t(x.keys) + 31) / 32 : 1;
+// Length of request r's units in steps of KEYS keys (a unit without keys still
+// has its rows to write), and how many there are.
+template <int KEYS>
+__device__ __forceinline__ int64_t unit_steps(const Request& x) {
+  return x.keys > 0 ? (int64_t(x.keys) + KEYS - 1) / KEYS : 1;
 }
 template <int ROWS>
 __device__ __forceinline__ int64_t unit_count(const DecodeArgs& A, const Request& x) {
   return int64_t(A.Hkv) * ((int64_t(x.qlen) * A.G.d + ROWS - 1) / ROWS);
 }
 
+// a / b, in 32 bits where both fit.
+__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : int64_t(uint32_t(a) / uint32_t(b));
+}
+
+// Resident CTAs per SM, by registers (168 and 255 a thread).
+__host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
+
 template <int D, int NG, int NT>
 struct Cfg {
   static constexpr int TILE = 16 * (D + 4 * NG);
   static constexpr int ROWS = 8 * NT;
   static constexpr int PITCH = D + 4;  // floats per row of the joining buffer
-  // Pairs of tiles in flight per warp: about 14 KB, so that 16 warps keep over
-  // 200 KB an SM in flight (copy rate times latency needs some 45 KB)
-  static constexpr int STAGES = D == 64 ? 6 : 3;
-  static constexpr int RING = STAGES * 2 * TILE;
+  // A warp takes TPS tiles (16 TPS keys) per step, as many as its registers
+  // hold scores of, and has ST steps' copies in flight: with 12 warps a SM some
+  // 200 KB (the copy rate times the latency needs about 45 KB).
+  static constexpr int TPS = NT == 1 ? 4 : 2;
+  static constexpr int ST = (NT == 1 ? 2 : 3) * (128 / D);
+  static constexpr int RING = ST * TPS * TILE;
   static constexpr int SMEM = kWarps * RING;
-  static constexpr int CTAS = NT == 1 ? 4 : 2;  // per SM, by registers
+  static constexpr int CTAS = ctas_per_sm(NT);
   static_assert(ROWS * PITCH * 4 <= RING, "a warp's result fits its ring");
-  static_assert(CTAS * (SMEM + 2048) <= 228 * 1024, "resident together");
+  static_assert(CTAS * (SMEM + 2816) <= 228 * 1024, "resident together");
 };
 
-// s_k or s_v of one token, float32.
+// The NG scales of one token's K or V, float32.
 template <int NG>
-__device__ __forceinline__ void load_scales(const uint8_t* at, float (&k)[NG], float (&v)[NG]) {
-  uint32_t w[NG];  // NG halves of K, NG of V
+__device__ __forceinline__ void load_scales(const uint8_t* at, float (&x)[NG]) {
   if constexpr (NG == 4) {
-    const uint4 x = *reinterpret_cast<const uint4*>(at);
-    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    const uint2 w = *reinterpret_cast<const uint2*>(at);
+    const float2 a = half2_f(w.x), b = half2_f(w.y);
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
   } else if constexpr (NG == 2) {
-    const uint2 x = *reinterpret_cast<const uint2*>(at);
-    w[0] = x.x, w[1] = x.y;
+    const float2 a = half2_f(*reinterpret_cast<const uint32_t*>(at));
+    x[0] = a.x, x[1] = a.y;
   } else {
-    w[0] = *reinterpret_cast<const uint32_t*>(at);
-  }
-  if constexpr (NG == 1) {
-    const float2 x = half2_f(w[0]);
-    k[0] = x.x, v[0] = x.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < NG / 2; ++i) {
-      const float2 x = half2_f(w[i]), y = half2_f(w[NG / 2 + i]);
-      k[2 * i] = x.x, k[2 * i + 1] = x.y;
-      v[2 * i] = y.x, v[2 * i + 1] = y.y;
-    }
+    x[0] = __half2float(*reinterpret_cast<const __half*>(at));
   }
 }
 
@@ -258,13 +255,16 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
   constexpr int J = D / 32;       // words of a token's codes per lane
   constexpr int JG = J / NG;      // of them per scale group
   constexpr int MT = D / 16;      // output row tiles
-  constexpr int ST = C::STAGES;
+  constexpr int ST = C::ST, TPS = C::TPS, KEYS = 16 * TPS;
+  constexpr int COST = kUnitKeys / KEYS;
+  constexpr int BATCH_STEPS = 32 / TPS;  // steps whose tile numbers a warp fetches at once
+  static_assert(ST < BATCH_STEPS, "steps in flight lie in two batches");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[kWarps][ST];
   __shared__ float2 s_ml[kWarps][C::ROWS];
   __shared__ int64_t s_scan[kWarps + 1];
   __shared__ int64_t s_found[2];
-  __shared__ int2 s_id[kWarps][2][16];  // tile numbers of a warp's next pairs, in two batches
+  __shared__ int32_t s_id[kWarps][2][32];  // tile numbers of a warp's next steps, two batches
   __shared__ int s_flag[2];  // a wait gave up; this CTA joins
   volatile int* abort = &s_flag[0];
 
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
   for (int r = r_lo; r < r_hi; ++r) {
     const Request x = request(A, r);
     const int64_t n = unit_count<C::ROWS>(A, x);
-    own += n * (unit_pairs(x) + kUnitCost);
+    own += n * (unit_steps<KEYS>(x) + COST);
     if (!x.sound && blockIdx.x == 0) atomicCAS(A.status, 0, int32_t(SPARGE_EINVAL));
   }
   int64_t incl = own;
@@ -306,18 +306,18 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
     total += s_scan[w];
   }
   before += incl - own;
-  // parts: a pair per warp at least
+  // parts: a step per warp at least
   int64_t parts = gridDim.x;
-  if (parts > (total + kWarps - 1) / kWarps) parts = (total + kWarps - 1) / kWarps;
+  parts = min(parts, (total + kWarps - 1) / kWarps);
   if (total == 0) return;
-  const int64_t step = (total + parts - 1) / parts;
+  const int64_t step = div64(total + parts - 1, parts);
   const int64_t line0 = blockIdx.x * step, line1 = min(line0 + step, total);
   if (line0 >= total) return;
   if (before <= line0 && line0 < before + own) {
     int64_t at = before;
     for (int r = r_lo; r < r_hi; ++r) {
       const Request x = request(A, r);
-      const int64_t n = unit_count<C::ROWS>(A, x) * (unit_pairs(x) + kUnitCost);
+      const int64_t n = unit_count<C::ROWS>(A, x) * (unit_steps<KEYS>(x) + COST);
       if (line0 < at + n) {
         s_found[0] = r;
         s_found[1] = at;
@@ -329,28 +329,28 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
   __syncthreads();
   int r = int(s_found[0]);
   int64_t r_at = s_found[1];  // where request r's units start
-  int put = 0, take = 0;      // stages that the next pair is copied to and taken from
+  int put = 0, take = 0;      // stages that the next step is copied to and taken from
   uint32_t phase = 0;         // parity of the stage `take`
   bool ok = true;
 
   for (int64_t line = line0; line < line1;) {
     Request req = request(A, r);
-    const int64_t n_pairs = unit_pairs(req), n_units = unit_count<C::ROWS>(A, req);
-    const int64_t length = n_pairs + kUnitCost;
+    const int64_t n_steps = unit_steps<KEYS>(req), n_units = unit_count<C::ROWS>(A, req);
+    const int64_t length = n_steps + COST;
     if (line >= r_at + n_units * length) {
       r_at += n_units * length;
       ++r;
       continue;
     }
     const int64_t into = line - r_at;
-    const int64_t unit = (into | length) >> 32 ? into / length : uint32_t(into) / uint32_t(length);
-    const int64_t pairs_at = r_at + unit * length + kUnitCost;  // where its first pair stands
-    const int pair0 = int(max(line - pairs_at, int64_t(0)));
-    const int64_t stop = min(line1, pairs_at + n_pairs);
-    const int pair1 = int(max(stop - pairs_at, int64_t(0)));
+    const int64_t unit = div64(into, length);
+    const int64_t steps_at = r_at + unit * length + COST;  // where its first step stands
+    const int step0 = int(max(line - steps_at, int64_t(0)));
+    const int64_t stop = min(line1, steps_at + n_steps);
+    const int step1 = int(max(stop - steps_at, int64_t(0)));
     line = stop;
-    if (pair1 == pair0) continue;  // the next CTA has all of it
-    const bool cut = pair0 > 0 || pair1 < n_pairs;
+    if (step1 == step0) continue;  // the next CTA has all of it
+    const bool cut = step0 > 0 || step1 < n_steps;
     const int tile_of = A.heads.quot(int(unit)), kvh = int(unit) - tile_of * A.Hkv;
     const int row0 = tile_of * C::ROWS, rows = req.qlen * int(A.G.d);
     // the last key that any row of this tile sees
@@ -358,16 +358,16 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
     const int32_t reach =
         A.causal ? min(req.keys, req.len - req.qlen + A.G.quot(last_row) + 1) : req.keys;
     const int n_tiles = reach > 0 ? (reach + 15) / 16 : 0;
-    const int n_here = min(pair1, (n_tiles + 1) / 2) - pair0;
-    // pair i of this warp is pair pair0 + warp + kWarps i of the unit
+    const int n_here = min(step1, (n_tiles + TPS - 1) / TPS) - step0;
+    // step i of this warp is step step0 + warp + kWarps i of the unit
     const int mine = n_here > warp ? (n_here - warp + kWarps - 1) / kWarps : 0;
 
-    // ---- the ring.  Tile numbers come in batches of 16 pairs, a lane to a tile:
-    // one batch in shared memory, the next in a register, fetched a batch ahead
+    // ---- the ring.  Tile numbers come in batches, a lane to a tile: one batch
+    // in shared memory, the next in a register, fetched a batch ahead
     const int32_t* table = A.table + int64_t(r) * A.max_pages;
     auto tile_id = [&](int batch) -> int32_t {
-      const int i = 16 * batch + (lane >> 1);
-      const int ti = 2 * (pair0 + warp + kWarps * i) + (lane & 1);
+      const int i = BATCH_STEPS * batch + lane / TPS;
+      const int ti = TPS * (step0 + warp + kWarps * i) + lane % TPS;
       if (i >= mine || ti >= n_tiles) return -1;
       const int32_t entry = A.tpp.quot(ti), page = __ldg(table + entry);
       if (uint32_t(page) >= uint32_t(A.num_pages)) {
@@ -376,37 +376,67 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
       }
       return (page * A.Hkv + kvh - entry) * int32_t(A.tpp.d) + ti;
     };
-    int32_t* ids = reinterpret_cast<int32_t*>(s_id[warp]);
-    ids[lane] = tile_id(0);
+    // where step i's tile numbers are
+    auto ids_of = [&](int i) {
+      return s_id[warp][i / BATCH_STEPS & 1] + TPS * (i % BATCH_STEPS);
+    };
+    s_id[warp][0][lane] = tile_id(0);
     int32_t next_id = tile_id(1);
     __syncwarp();
     auto issue = [&](int i) {
       if (i >= mine) return;
-      if (i > 0 && (i & 15) == 0) {
-        // at most ST < 16 pairs are still to be taken: none of the batch that goes
-        ids[(i & 16) * 2 + lane] = next_id;
-        next_id = tile_id((i >> 4) + 1);
+      if (i > 0 && i % BATCH_STEPS == 0) {
+        // the steps still to be taken lie in the batch before: its place is the other
+        ids_of(i)[lane] = next_id;
+        next_id = tile_id(i / BATCH_STEPS + 1);
         __syncwarp();
       }
       if (lane == 0) {
-        const int2 id = s_id[warp][i >> 4 & 1][i & 15];
+        int32_t id[TPS];
+        const int32_t* at = ids_of(i);
+        bool run = true;  // all there, and one behind the other in memory
+        int n = 0;
+#pragma unroll
+        for (int u = 0; u < TPS; ++u) {
+          id[u] = at[u];
+          n += id[u] >= 0;
+          run = run && id[u] == id[0] + u;
+        }
         uint64_t* bar = &full[warp][put];
-        uint8_t* dst = ring + put * 2 * C::TILE;
-        const uint8_t* src = A.cache + int64_t(id.x) * C::TILE;
-        if (id.x >= 0 && id.y == id.x + 1) {  // neighbours in one page
-          mbar_expect_tx(bar, 2 * C::TILE);
-          bulk_load(dst, src, 2 * C::TILE, bar);
-        } else if (id.x >= 0 || id.y >= 0) {
-          mbar_expect_tx(bar, (id.x >= 0 && id.y >= 0 ? 2 : 1) * C::TILE);
-          if (id.x >= 0) bulk_load(dst, src, C::TILE, bar);
-          if (id.y >= 0)
-            bulk_load(dst + C::TILE, A.cache + int64_t(id.y) * C::TILE, C::TILE, bar);
+        uint8_t* dst = ring + put * TPS * C::TILE;
+        if (run && id[0] >= 0) {
+          mbar_expect_tx(bar, TPS * C::TILE);
+          bulk_load(dst, A.cache + int64_t(id[0]) * C::TILE, TPS * C::TILE, bar);
+        } else if (n > 0) {
+          mbar_expect_tx(bar, n * C::TILE);
+#pragma unroll
+          for (int u = 0; u < TPS; ++u)
+            if (id[u] >= 0)
+              bulk_load(dst + u * C::TILE, A.cache + int64_t(id[u]) * C::TILE, C::TILE, bar);
         } else {
           mbar_arrive(bar);  // nothing to copy: these keys are left out
         }
       }
       put = put + 1 == ST ? 0 : put + 1;
     };
+    // The queries are asked for before the copies: behind 30 MB of those, at the
+    // launch's start, they took 5 us.
+    uint4 raw_q[NT][J];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = row0 + 8 * nt + g;
+      const bool there = row < rows;
+#pragma unroll
+      for (int j = 0; j < J; ++j) raw_q[nt][j] = make_uint4(0, 0, 0, 0);
+      if (there) {
+        const int tok = A.G.quot(row), head = kvh * int(A.G.d) + row - tok * int(A.G.d);
+        const char* src =
+            A.q + int64_t(req.q0 + tok) * A.q_stride + int64_t(head) * (D * 2) + 16 * t;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          raw_q[nt][j] = *reinterpret_cast<const uint4*>(src + 64 * j);
+      }
+    }
     if (ok) {
 #pragma unroll
       for (int i = 0; i < ST; ++i) issue(i);
@@ -415,22 +445,17 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
     // ---- Q as B fragments: column g is query row row0 + 8 nt + g; the 32-bit
     // word (t, j) of a token's codes meets channels 32 j + 8 t .. + 7
     uint32_t qf[NT][2 * J][2];
+    float start[NT][NG][2];  // -72 times the sum of the channels at bits 4-7, columns 2t, 2t + 1
     float f[NT][2];        // score of a column: f * sum_g s_g S_g, in log2 units
     int32_t lim[NT][2];    // the column sees keys below this
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = row0 + 8 * nt + g;
-      const bool there = row < rows;
-      const int tok = there ? A.G.quot(row) : 0;
-      const int head = kvh * int(A.G.d) + (there ? row - tok * int(A.G.d) : 0);
-      const char* src = A.q + int64_t(req.q0 + tok) * A.q_stride + int64_t(head) * (D * 2);
       float x[J][8];
       float big = 0.f;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (there) raw = *reinterpret_cast<const uint4*>(src + (32 * j + 8 * t) * 2);
-        const uint32_t* u = reinterpret_cast<const uint32_t*>(&raw);
+        const uint4 raw = raw_q[nt][j];
+        const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (A.bf16) {
@@ -452,12 +477,29 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
       const int k = field < 255 ? 139 - field : 0, half_k = k >> 1;
       const auto two_to = [](int n) { return __uint_as_float(uint32_t(n + 127) << 23); };
       const float k1 = two_to(half_k), k2 = two_to(k - half_k);
+      float sum[NG];
 #pragma unroll
-      for (int j = 0; j < J; ++j)
+      for (int n = 0; n < NG; ++n) sum[n] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          qf[nt][2 * j + i / 2][i & 1] =
-              pack_half2(x[j][2 * i] * k1 * k2, x[j][2 * i + 1] * k1 * k2);
+      for (int j = 0; j < J; ++j) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t h = pack_half2(x[j][2 * i] * k1 * k2, x[j][2 * i + 1] * k1 * k2);
+          qf[nt][2 * j + i / 2][i & 1] = h;
+          if (i & 1) {
+            const float2 back = half2_f(h);
+            sum[j / JG] += back.x + back.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], 1);
+        sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], 2);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          start[nt][n][c] = -72.0f * __shfl_sync(0xffffffffu, sum[n], (2 * t + c) * 4);
+      }
       const float fr = A.scale_log2 * two_to(-half_k) * two_to(half_k - k);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -491,23 +533,24 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
       if (!ok) break;
       take = take + 1 == ST ? 0 : take + 1;
       phase ^= take == 0;
-      const uint8_t* pair = ring + stage * 2 * C::TILE;
-      const int32_t key0 = (pair0 + warp + kWarps * i) * 32;
-      const int2 id = s_id[warp][i >> 4 & 1][i & 15];
+      const uint8_t* tiles = ring + stage * TPS * C::TILE;
+      const int32_t key0 = (step0 + warp + kWarps * i) * KEYS;
+      uint32_t here = 0;  // bit u: tile u was copied
+      {
+        const int32_t* at = ids_of(i);
+#pragma unroll
+        for (int u = 0; u < TPS; ++u) here |= uint32_t(at[u] >= 0) << u;
+      }
 
-      // One pair; MASKED: some row does not see some key of it.
+      // One step; MASKED: some row does not see some key of it.
       auto step = [&](auto masked) {
         constexpr bool MASKED = decltype(masked)::value;
-        float s[2][NT][4], sv[2][2][NG];
+        float s[TPS][NT][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint8_t* tile = pair + u * C::TILE;
-          float sk[2][NG];  // tokens g and g + 8
-#pragma unroll
-          for (int a = 0; a < 2; ++a)
-            load_scales<NG>(tile + 16 * D + (g + 8 * a) * NG * 4, sk[a], sv[u][a]);
+        for (int u = 0; u < TPS; ++u) {
+          const uint8_t* tile = tiles + u * C::TILE;
           // ---- S^T
-          uint32_t ka[J], kb[J];
+          uint32_t ka[J], kb[J];  // tokens g and g + 8
           if constexpr (J == 4) {
             const uint4 wa = *reinterpret_cast<const uint4*>(tile + g * (D / 2) + t * 16);
             const uint4 wb = *reinterpret_cast<const uint4*>(tile + (g + 8) * (D / 2) + t * 16);
@@ -519,23 +562,25 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
             ka[0] = wa.x, ka[1] = wa.y;
             kb[0] = wb.x, kb[1] = wb.y;
           }
+          float sk[2][NG];
+          load_scales<NG>(tile + 16 * D + g * NG * 4, sk[0]);
+          load_scales<NG>(tile + 16 * D + (g + 8) * NG * 4, sk[1]);
 #pragma unroll
           for (int n = 0; n < NG; ++n) {
             float acc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              acc[nt][0] = acc[nt][2] = start[nt][n][0], acc[nt][1] = acc[nt][3] = start[nt][n][1];
 #pragma unroll
             for (int j = n * JG; j < (n + 1) * JG; ++j) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const uint32_t wa = ka[j] >> (8 * h), wb = kb[j] >> (8 * h);
                 const uint32_t a0 = codes0(wa, masks), a1 = codes0(wb, masks);
-                const uint32_t a2 = codes4(wa, masks), a3 = codes4(wb, masks);
+                const uint32_t a2 = raised4(wa, masks), a3 = raised4(wb, masks);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  if (j == n * JG && h == 0)
-                    mma16816_zero(acc[nt], a0, a1, a2, a3, qf[nt][2 * j][0], qf[nt][2 * j][1]);
-                  else
-                    mma16816(acc[nt], a0, a1, a2, a3, qf[nt][2 * j + h][0], qf[nt][2 * j + h][1]);
-                }
+                for (int nt = 0; nt < NT; ++nt)
+                  mma16816(acc[nt], a0, a1, a2, a3, qf[nt][2 * j + h][0], qf[nt][2 * j + h][1]);
               }
             }
 #pragma unroll
@@ -553,18 +598,18 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
             for (int c = 0; c < 4; ++c) s[u][nt][c] *= f[nt][c & 1];
         }
         // ---- keys that a row does not see
-        uint32_t seen = ~0u;  // bit 16 u + 4 nt + c
+        uint32_t seen = ~0u;  // bit 4 (NT u + nt) + c
         if (MASKED) {
           seen = 0;
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < TPS; ++u)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 const bool yes =
-                    (u == 0 ? id.x : id.y) >= 0 && key0 + 16 * u + g + 8 * (c >> 1) < lim[nt][c & 1];
-                seen |= uint32_t(yes) << (16 * u + 4 * nt + c);
+                    (here >> u & 1u) && key0 + 16 * u + g + 8 * (c >> 1) < lim[nt][c & 1];
+                seen |= uint32_t(yes) << (4 * (NT * u + nt) + c);
                 if (!yes) s[u][nt][c] = -INFINITY;
               }
         }
@@ -575,9 +620,11 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            high[nt][c] =
-                fmaxf(max3(s[0][nt][c], s[0][nt][c + 2], s[1][nt][c]), s[1][nt][c + 2]);
-            raise |= high[nt][c] > m[nt][c] + kLazy;
+            float x = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
+#pragma unroll
+            for (int u = 1; u < TPS; ++u) x = max3(x, s[u][nt][c], s[u][nt][c + 2]);
+            high[nt][c] = x;
+            raise |= x > m[nt][c] + kLazy;
           }
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -597,8 +644,11 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
           }
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint8_t* tile = pair + u * C::TILE;
+        for (int u = 0; u < TPS; ++u) {
+          const uint8_t* tile = tiles + u * C::TILE;
+          float sv[2][NG];
+          load_scales<NG>(tile + 16 * D + g * NG * 4 + 2 * NG, sv[0]);
+          load_scales<NG>(tile + 16 * D + (g + 8) * NG * 4 + 2 * NG, sv[1]);
           // ---- weights, times V's scales, as B fragments (rows = keys)
           uint32_t pf[NT][NG][2];
 #pragma unroll
@@ -607,7 +657,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               p[c] = ex2_approx(s[u][nt][c] - m[nt][c & 1]);
-              if (MASKED && !(seen >> (16 * u + 4 * nt + c) & 1)) p[c] = 0.f;
+              if (MASKED && !(seen >> (4 * (NT * u + nt) + c) & 1)) p[c] = 0.f;
             }
             l[nt][0] += p[0] + p[2];
             l[nt][1] += p[1] + p[3];
@@ -616,9 +666,9 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
               float w[4];
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                w[c] = p[c] * sv[u][c >> 1][n];
+                w[c] = p[c] * sv[c >> 1][n];
                 // a key that is not seen counts nothing, whatever its scale is
-                if (MASKED && !(seen >> (16 * u + 4 * nt + c) & 1)) w[c] = 0.f;
+                if (MASKED && !(seen >> (4 * (NT * u + nt) + c) & 1)) w[c] = 0.f;
               }
               pf[nt][n][0] = transpose8x8(pack_half2(w[0], w[1]));
               pf[nt][n][1] = transpose8x8(pack_half2(w[2], w[3]));
@@ -646,7 +696,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
           }
         }
       };
-      if (id.x >= 0 && id.y >= 0 && key0 + 32 <= all_see)
+      if (here == (1u << TPS) - 1 && key0 + KEYS <= all_see)
         step(std::false_type{});
       else
         step(std::true_type{});
@@ -685,7 +735,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
     __syncthreads();
 
     // ---- the warps joined: finished, or this CTA's part of a cut unit
-    const int64_t slot = 2 * int64_t(blockIdx.x) + (pair0 > 0 ? 0 : 1);
+    const int64_t slot = 2 * int64_t(blockIdx.x) + (step0 > 0 ? 0 : 1);
     const int here_rows = min(C::ROWS, rows - row0);
     auto join_warps = [&](bool finish) {
       for (int e = threadIdx.x; e < here_rows * (D / 2); e += kAttnThreads) {
@@ -721,8 +771,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
 
     // ---- the last of a cut unit's CTAs joins its parts: a warp each fourth of
     // them, in their order, then the warps as above
-    const int64_t c0 = pair0 == 0 ? blockIdx.x : pairs_at / step;
-    const int n_parts = int((pairs_at + n_pairs - 1) / step - c0) + 1;
+    const int64_t c0 = step0 == 0 ? int64_t(blockIdx.x) : div64(steps_at, step);
+    const int n_parts = int(div64(steps_at + n_steps - 1, step) - c0) + 1;
     if (threadIdx.x == 0)
       s_flag[1] = atomicInc(A.arrived + c0, uint32_t(n_parts - 1)) == uint32_t(n_parts - 1);
     __syncthreads();
@@ -731,59 +781,69 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
     constexpr int V = 4;                   // channels per lane
     constexpr int RPW = 32 * V / D;        // rows that a warp's load covers
     constexpr int ITEMS = C::ROWS / RPW;
-    constexpr int BATCH = NT == 1 ? 4 : 2;  // parts in flight
+    constexpr int EG = ITEMS < 4 ? ITEMS : 4, BATCH = 4;  // rows and parts in flight
     const int ch = V * lane % D, sub = V * lane / D;
-    float top[ITEMS], sum[ITEMS], x[ITEMS][V];
+#pragma unroll 1
+    for (int e0 = 0; e0 < ITEMS && e0 * RPW < here_rows; e0 += EG) {
+      float top[EG], sum[EG], x[EG][V];
 #pragma unroll
-    for (int e = 0; e < ITEMS; ++e) {
-      top[e] = kLow, sum[e] = 0.f;
+      for (int e = 0; e < EG; ++e) {
+        top[e] = kLow, sum[e] = 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) x[e][v] = 0.f;
-    }
-    for (int k0 = warp; k0 < n_parts; k0 += kWarps * BATCH) {
-#pragma unroll
-      for (int e = 0; e < ITEMS; ++e) {
-        const int row = e * RPW + sub;
-        if (e * RPW >= here_rows) break;
-        float2 ml[BATCH];
-        float4 q[BATCH];
+        for (int v = 0; v < V; ++v) x[e][v] = 0.f;
+      }
+#pragma unroll 1
+      for (int k0 = warp; k0 < n_parts; k0 += kWarps * BATCH) {
+        float2 ml[BATCH][EG];
+        float4 q[BATCH][EG];
+        // loads without conditions, so that all are in flight: behind the last
+        // part or row they repeat it, and count nothing
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
-          const int k = k0 + kWarps * i;
-          ml[i] = make_float2(kLow, 0.f);
-          q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (k < n_parts && row < here_rows) {
-            // the first part is its CTA's last unit, the others are their CTAs' first
-            const int64_t at = (2 * (c0 + k) + (k == 0 ? 1 : 0)) * C::ROWS + row;
-            ml[i] = __ldcg(A.part_ml + at);
-            q[i] = __ldcg(reinterpret_cast<const float4*>(A.part_o + at * D + ch));
+          const int k = min(k0 + kWarps * i, n_parts - 1);
+          // the first part is its CTA's last unit, the others are their CTAs' first
+          const int64_t at = (2 * (c0 + k) + (k == 0 ? 1 : 0)) * C::ROWS;
+#pragma unroll
+          for (int e = 0; e < EG; ++e) {
+            const int64_t row = at + min((e0 + e) * RPW + sub, here_rows - 1);
+            ml[i][e] = __ldcg(A.part_ml + row);
+            q[i][e] = __ldcg(reinterpret_cast<const float4*>(A.part_o + row * D + ch));
           }
         }
-        float now = top[e];
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) now = fmaxf(now, ml[i].x);
-        const float old = ex2_approx(top[e] - now);
-        top[e] = now;
-        sum[e] *= old;
+        for (int i = 0; i < BATCH; ++i)
+          if (k0 + kWarps * i >= n_parts) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) x[e][v] *= old;
+            for (int e = 0; e < EG; ++e) ml[i][e] = make_float2(-INFINITY, 0.f);
+          }
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-          const float a = ex2_approx(ml[i].x - now);
-          sum[e] = fmaf(ml[i].y, a, sum[e]);
-          x[e][0] = fmaf(q[i].x, a, x[e][0]);
-          x[e][1] = fmaf(q[i].y, a, x[e][1]);
-          x[e][2] = fmaf(q[i].z, a, x[e][2]);
-          x[e][3] = fmaf(q[i].w, a, x[e][3]);
+        for (int e = 0; e < EG; ++e) {
+          float now = top[e];
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) now = fmaxf(now, ml[i][e].x);
+          const float old = ex2_approx(top[e] - now);
+          top[e] = now;
+          sum[e] *= old;
+#pragma unroll
+          for (int v = 0; v < V; ++v) x[e][v] *= old;
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const float a = ex2_approx(ml[i][e].x - now);
+            sum[e] = fmaf(ml[i][e].y, a, sum[e]);
+            x[e][0] = fmaf(q[i][e].x, a, x[e][0]);
+            x[e][1] = fmaf(q[i][e].y, a, x[e][1]);
+            x[e][2] = fmaf(q[i][e].z, a, x[e][2]);
+            x[e][3] = fmaf(q[i][e].w, a, x[e][3]);
+          }
         }
       }
-    }
 #pragma unroll
-    for (int e = 0; e < ITEMS; ++e) {
-      const int row = e * RPW + sub;
-      *reinterpret_cast<float4*>(so + row * C::PITCH + ch) =
-          make_float4(x[e][0], x[e][1], x[e][2], x[e][3]);
-      if (ch == 0) s_ml[warp][row] = make_float2(top[e], sum[e]);
+      for (int e = 0; e < EG; ++e) {
+        const int row = (e0 + e) * RPW + sub;
+        *reinterpret_cast<float4*>(so + row * C::PITCH + ch) =
+            make_float4(x[e][0], x[e][1], x[e][2], x[e][3]);
+        if (ch == 0) s_ml[warp][row] = make_float2(top[e], sum[e]);
+      }
     }
     __syncthreads();
     join_warps(true);
@@ -797,15 +857,15 @@ struct Plan {
 };
 
 // CTAs from the bounds that the host knows (lengths are on the device): all
-// that are resident at once, fewer when there cannot be a pair for each warp.
+// that are resident at once, fewer when there cannot be a step for each warp.
 Plan make_plan(const sparge_kv4_t& c, const sparge_kv4_attn_t& a) {
   Plan p{};
   const int64_t rows = int64_t(a.max_q) * (a.Hq / c.Hkv);
   p.nt = rows <= 8 ? 1 : 2;
-  const int64_t pairs = cdiv(kv4_len_cap(c, a), 32);
-  const int64_t most = kSms * (p.nt == 1 ? 4 : 2);
-  // more than `most` pairs per request and head already: no need to multiply on
-  int64_t line = pairs < 1 ? 1 : pairs;
+  const int64_t steps = cdiv(kv4_len_cap(c, a), p.nt == 1 ? 64 : 32);
+  const int64_t most = kSms * ctas_per_sm(p.nt);
+  // more than that many CTAs' steps already: no need to multiply on
+  int64_t line = steps < 1 ? 1 : steps;
   const int64_t by[] = {cdiv(rows, 8 * p.nt), c.Hkv, a.R};
   for (int64_t n : by) line = line > most * kWarps ? line : line * (n < 1 ? 1 : n);
   const int64_t grid = cdiv(line, kWarps);
@@ -815,13 +875,14 @@ Plan make_plan(const sparge_kv4_t& c, const sparge_kv4_attn_t& a) {
 
 // Of one size for every call, so that calls of different shapes may share a
 // workspace: no other region ever lies on the counters.
-size_t arrived_bytes(const Plan&) { return align256(size_t(kSms) * 4 * sizeof(uint32_t)); }
+size_t arrived_bytes(const Plan&) {
+  return align256(size_t(kSms) * ctas_per_sm(1) * sizeof(uint32_t));
+}
 size_t ml_bytes(const Plan& p) { return align256(size_t(p.grid) * 2 * 8 * p.nt * sizeof(float2)); }
 
 template <int D, int NG, int NT>
 cudaError_t run(const DecodeArgs& a, const Plan& p, cudaStream_t stream) {
   using C = Cfg<D, NG, NT>;
-  static_assert(kSms * C::CTAS == (NT == 1 ? kSms * 4 : kSms * 2), "as make_plan counts");
   const cudaError_t e = cudaFuncSetAttribute(
       kv4_attn_kernel<D, NG, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
