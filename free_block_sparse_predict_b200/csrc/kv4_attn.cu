@@ -18,7 +18,9 @@
 // align sums by the exponent field: measured, that cost seven bits of them.)
 //
 // Scales: S is summed per group in float32, S = sum_g s_g S_g.  V's scale
-// goes into the weights, p s rounded to fp16 once.  Q is fp16 with one power
+// goes into the weights: p is rounded to fp16 and p s once more (the sum of
+// weights is of the unrounded p; both roundings are far below the 4 bits' own
+// and together about the output's, and save a tenth of the instructions).  Q is fp16 with one power
 // of two per row, so bf16 queries lose nothing above 2^-26 of the row's
 // largest.  The running maximum is lazy: it is raised (and O rescaled) when a
 // score passes it by more than 2 in log2 units, so weights stay below 4 and
@@ -123,6 +125,11 @@ __device__ __forceinline__ uint32_t minus(uint32_t x, uint32_t y) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(y));
   return d;
 }
+__device__ __forceinline__ uint32_t times(uint32_t x, uint32_t y) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(y));
+  return d;
+}
 // (w & mask) | magic; a LOP3 takes one immediate, so the mask is in a register
 // whose value the compiler does not know (it would make two instructions of it)
 __device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t mask, uint32_t magic) {
@@ -135,12 +142,6 @@ __device__ __forceinline__ uint32_t codes0(uint32_t w, const Masks& k) {
 }
 __device__ __forceinline__ uint32_t codes4(uint32_t w, const Masks& k) {
   return minus(pick(w, k.high, 0x54005400u), 0x54805480u);  // 64 + u, 72
-}
-// The same with the 72 left on: K's sums start at -72 times the sum of those
-// channels of Q instead (exact numbers of 4.5 times the codes' size: their
-// float32 sums lose two bits more, which 2^-22 allows).
-__device__ __forceinline__ uint32_t raised4(uint32_t w, const Masks& k) {
-  return pick(w, k.high, 0x54005400u);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -223,6 +224,22 @@ __device__ __forceinline__ void load_scales(const uint8_t* at, float (&x)[NG]) {
     x[0] = a.x, x[1] = a.y;
   } else {
     x[0] = __half2float(*reinterpret_cast<const __half*>(at));
+  }
+}
+
+// The same as fp16, each in both halves of a word.
+template <int NG>
+__device__ __forceinline__ void load_scales_twice(const uint8_t* at, uint32_t (&x)[NG]) {
+  if constexpr (NG == 4) {
+    const uint2 w = *reinterpret_cast<const uint2*>(at);
+    x[0] = __byte_perm(w.x, w.x, 0x1010), x[1] = __byte_perm(w.x, w.x, 0x3232);
+    x[2] = __byte_perm(w.y, w.y, 0x1010), x[3] = __byte_perm(w.y, w.y, 0x3232);
+  } else if constexpr (NG == 2) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(at);
+    x[0] = __byte_perm(w, w, 0x1010), x[1] = __byte_perm(w, w, 0x3232);
+  } else {
+    const uint32_t w = *reinterpret_cast<const uint16_t*>(at);
+    x[0] = __byte_perm(w, w, 0x1010);
   }
 }
 
@@ -445,7 +462,6 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
     // ---- Q as B fragments: column g is query row row0 + 8 nt + g; the 32-bit
     // word (t, j) of a token's codes meets channels 32 j + 8 t .. + 7
     uint32_t qf[NT][2 * J][2];
-    float start[NT][NG][2];  // -72 times the sum of the channels at bits 4-7, columns 2t, 2t + 1
     float f[NT][2];        // score of a column: f * sum_g s_g S_g, in log2 units
     int32_t lim[NT][2];    // the column sees keys below this
 #pragma unroll
@@ -477,29 +493,12 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
       const int k = field < 255 ? 139 - field : 0, half_k = k >> 1;
       const auto two_to = [](int n) { return __uint_as_float(uint32_t(n + 127) << 23); };
       const float k1 = two_to(half_k), k2 = two_to(k - half_k);
-      float sum[NG];
 #pragma unroll
-      for (int n = 0; n < NG; ++n) sum[n] = 0.f;
+      for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t h = pack_half2(x[j][2 * i] * k1 * k2, x[j][2 * i + 1] * k1 * k2);
-          qf[nt][2 * j + i / 2][i & 1] = h;
-          if (i & 1) {
-            const float2 back = half2_f(h);
-            sum[j / JG] += back.x + back.y;
-          }
-        }
-      }
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], 1);
-        sum[n] += __shfl_xor_sync(0xffffffffu, sum[n], 2);
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          start[nt][n][c] = -72.0f * __shfl_sync(0xffffffffu, sum[n], (2 * t + c) * 4);
-      }
+        for (int i = 0; i < 4; ++i)
+          qf[nt][2 * j + i / 2][i & 1] =
+              pack_half2(x[j][2 * i] * k1 * k2, x[j][2 * i + 1] * k1 * k2);
       const float fr = A.scale_log2 * two_to(-half_k) * two_to(half_k - k);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -570,14 +569,15 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
             float acc[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              acc[nt][0] = acc[nt][2] = start[nt][n][0], acc[nt][1] = acc[nt][3] = start[nt][n][1];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) acc[nt][c] = 0.f;
 #pragma unroll
             for (int j = n * JG; j < (n + 1) * JG; ++j) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const uint32_t wa = ka[j] >> (8 * h), wb = kb[j] >> (8 * h);
                 const uint32_t a0 = codes0(wa, masks), a1 = codes0(wb, masks);
-                const uint32_t a2 = raised4(wa, masks), a3 = raised4(wb, masks);
+                const uint32_t a2 = codes4(wa, masks), a3 = codes4(wb, masks);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                   mma16816(acc[nt], a0, a1, a2, a3, qf[nt][2 * j + h][0], qf[nt][2 * j + h][1]);
@@ -646,9 +646,9 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
 #pragma unroll
         for (int u = 0; u < TPS; ++u) {
           const uint8_t* tile = tiles + u * C::TILE;
-          float sv[2][NG];
-          load_scales<NG>(tile + 16 * D + g * NG * 4 + 2 * NG, sv[0]);
-          load_scales<NG>(tile + 16 * D + (g + 8) * NG * 4 + 2 * NG, sv[1]);
+          uint32_t sv[2][NG];  // of tokens g and g + 8, twice in a word
+          load_scales_twice<NG>(tile + 16 * D + g * NG * 4 + 2 * NG, sv[0]);
+          load_scales_twice<NG>(tile + 16 * D + (g + 8) * NG * 4 + 2 * NG, sv[1]);
           // ---- weights, times V's scales, as B fragments (rows = keys)
           uint32_t pf[NT][NG][2];
 #pragma unroll
@@ -661,17 +661,18 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
             }
             l[nt][0] += p[0] + p[2];
             l[nt][1] += p[1] + p[3];
+            const uint32_t pa = pack_half2(p[0], p[1]), pb = pack_half2(p[2], p[3]);
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-              float w[4];
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                w[c] = p[c] * sv[c >> 1][n];
+              uint32_t wa = times(pa, sv[0][n]), wb = times(pb, sv[1][n]);
+              if (MASKED) {
                 // a key that is not seen counts nothing, whatever its scale is
-                if (MASKED && !(seen >> (4 * (NT * u + nt) + c) & 1)) w[c] = 0.f;
+                const uint32_t bits = seen >> (4 * (NT * u + nt));
+                wa &= (bits & 1 ? 0xFFFFu : 0u) | (bits & 2 ? 0xFFFF0000u : 0u);
+                wb &= (bits & 4 ? 0xFFFFu : 0u) | (bits & 8 ? 0xFFFF0000u : 0u);
               }
-              pf[nt][n][0] = transpose8x8(pack_half2(w[0], w[1]));
-              pf[nt][n][1] = transpose8x8(pack_half2(w[2], w[3]));
+              pf[nt][n][0] = transpose8x8(wa);
+              pf[nt][n][1] = transpose8x8(wb);
             }
           }
           // ---- O^T

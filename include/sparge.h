@@ -358,7 +358,7 @@ size_t sparge_kv4_workspace_bytes(const sparge_kv4_t* c, const sparge_kv4_attn_t
  *     leaves them
  *   o    [T, Hq, d] of dtype; lse: nullable float32 [T, Hq], log of the sum of exponentials
  * Q is taken to fp16 with one power of two per row, products accumulate in float32, softmax
- * statistics are float32, and weight times V's scale is rounded to fp16 once.
+ * statistics are float32; a weight, and its product with V's scale, are rounded to fp16.
  * Keys at pages outside [0, num_pages) or behind max_len are left out; these, a length below
  * 0 and a cu_q that does not ascend within [0, T] by steps of at most max_q (such a request
  * is skipped) put SPARGE_EINVAL into the workspace's status word (sparge_device_status).

@@ -256,8 +256,8 @@ def check_attn(case, got, want):
     sum |q_g| and s_g = max|k_g| / 7; with the group sums and the exponent's own argument below
     2^-17 E.  exp2 and the (at most some twenty) rescalings and joins, 2^-22 each: 2^-17.  So a
     weight and the sum of weights are each off by w = 2^-17 (E + 1), relatively, and lse by as
-    much.  p s is rounded to fp16 once: 2^-11 sum p |v|, and below fp16's normal range 2^-25 a
-    key, times a code of up to 7 (the sum of weights is at least 1): 6 standard deviations of n
+    much.  p is rounded to fp16 and p s again: 2^-10 sum p |v|, and below fp16's normal range
+    2^-25 (1 + s) a key, s up to max |v| / 7, times a code of up to 7 (the sum of weights is at least 1): 6 standard deviations of n
     independent ones.  Sums of up to max |v| in n/64 (at most 512) steps a warp, each off by
     2^-22 of them.  Then the output's rounding."""
     (o, lse), (wo, wl, size, err, keys) = got, want
@@ -265,8 +265,8 @@ def check_attn(case, got, want):
     w = 2.0 ** -17 * (err + 1)
     vmax = float(case.v.abs().nan_to_num(0, 0, 0).max()) if case.v.numel() else 0.0
     steps = (keys / 64).clamp(max=512) + 2
-    tol = (2.0 ** -11 + 2 * w)[..., None] * size + \
-        (6 * 7 * 2.0 ** -25 * keys.sqrt() + steps * 2.0 ** -22 * vmax)[..., None]
+    tol = (2.0 ** -10 + 2 * w)[..., None] * size + \
+        (6 * (7 + vmax) * 2.0 ** -25 * keys.sqrt() + steps * 2.0 ** -22 * vmax)[..., None]
     tol = tol * (1 + 2.0 ** -8) + torch.finfo(o.dtype).eps / 2 * wo.abs() + 2.0 ** -25
     d = (o[:n].double() - wo[:n]).abs()
     assert bool((d <= tol[:n]).all()), (float((d - tol[:n]).max()), float(d.max()))
