@@ -6,9 +6,14 @@
 // HBM-bound: append reads 4d bytes of K and V per token and head and writes
 // d + 4 d/group; read is the other way round.
 //
-// A row of d channels is held by d/8 lanes, eight channels each, K's row by
-// the lower half of 2 d/8 lanes and V's by the upper: a warp holds one (d =
-// 128) or two (d = 64) token-heads.
+// A CTA takes 16 rows of two (d = 128) or four heads, usually one tile of each,
+// at most parts of 16.  A row of d channels is held by d/8 lanes, eight channels
+// each, K's row by the lower half of 2 d/8 lanes and V's by the upper, and every
+// thread has four such pieces in flight.  K's codes of a token lie together and
+// are stored as they are; V's lie 64 bytes apart, next to those of the tile's
+// other tokens, so append gathers them in shared memory and stores them in the
+// cache's order, and read takes them as the words they are, from L1 after the
+// first token, and exchanges their bytes among the lanes.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -38,42 +43,102 @@ struct CacheArgs {
   const int32_t* slots;
   uint8_t* cache;
   int32_t* status;
-  int64_t items;  // T * Hkv
-  int32_t slots_end;  // num_pages * page_size
+  int32_t T, slots_end;  // slots_end: num_pages * page_size
   int32_t Hkv, page, tpp, dtype;  // tpp: tiles per page
 };
 
-// Where a (token, head) lives: its tile's address and its place in the tile.
-__device__ __forceinline__ uint8_t* tile_of(const CacheArgs& A, int32_t slot, int32_t head,
-                                            int32_t tile_bytes, int* tok) {
+constexpr int kRows = 16;    // rows per CTA
+constexpr int kPasses = 4;   // pieces per thread
+
+template <int D>
+struct CacheCfg {
+  static constexpr int LANES = D / 8;                          // lanes per row
+  static constexpr int PER_PASS = kCacheThreads / (2 * LANES);  // token-heads per pass
+  static constexpr int HEADS = kPasses * PER_PASS / kRows;
+};
+
+// The CTA's slots: threads 0..15 find each row's tile of KV head 0 (a tile
+// number; a head on is tpp tiles on) and its place in it, -1 for rows to skip.
+__device__ __forceinline__ int32_t find_slot(const CacheArgs& A, int32_t t, int64_t* tile) {
+  int32_t slot = t < A.T ? A.slots[t] : -1;
+  if (uint32_t(slot) >= uint32_t(A.slots_end)) return -1;
   const int32_t page = slot / A.page, in = slot - page * A.page;
-  *tok = in & 15;
-  return A.cache + (((int64_t(page) * A.Hkv + head) * A.tpp) + (in >> 4)) * tile_bytes;
+  *tile = int64_t(page) * A.Hkv * A.tpp + (in >> 4);
+  return slot;
 }
+// A token's place in its tile: pages hold whole tiles.
+__device__ __forceinline__ int token_of(int32_t slot) { return slot & 15; }
 
-template <int D, int NG>
+// Where a thread's piece of pass p stands: rows and heads behind its first.
+template <int D>
+struct Piece {
+  static __device__ __forceinline__ constexpr int row(int p) {
+    return p * CacheCfg<D>::PER_PASS % kRows;
+  }
+  static __device__ __forceinline__ constexpr int head(int p) {
+    return p * CacheCfg<D>::PER_PASS / kRows;
+  }
+};
+
+template <int D, int NG, int DT>
 __global__ void __launch_bounds__(kCacheThreads) append_kernel(const CacheArgs A) {
-  constexpr int LANES = D / 8;        // lanes per row
+  using C = CacheCfg<D>;
+  constexpr int LANES = C::LANES;
   constexpr int GL = D / NG / 8;      // lanes per scale group
+  constexpr int WORDS = D / 8;        // 32-bit words of V's codes per token
+  constexpr int PITCH = kRows + 1;
   constexpr Kv4Tile L{D, NG};
-  const int64_t thread = int64_t(blockIdx.x) * kCacheThreads + threadIdx.x;
-  const int64_t item = thread / (2 * LANES);
-  const bool is_v = (threadIdx.x / LANES) & 1;
-  const int lane = threadIdx.x % LANES;
-  const int32_t t = int32_t(item / A.Hkv), head = int32_t(item - int64_t(t) * A.Hkv);
-  const int32_t slot = item < A.items ? A.slots[t] : -1;
-  const bool there = uint32_t(slot) < uint32_t(A.slots_end);
+  __shared__ int32_t s_slot[kRows];
+  __shared__ int64_t s_tile[kRows];
+  __shared__ int8_t s_order[kRows];   // rows in the order of their words in the cache
+  __shared__ uint32_t s_v[C::HEADS][WORDS][PITCH];
+  __shared__ __align__(16) __half s_scale[C::HEADS][kRows][2 * NG];
 
-  float x[8];
+  const int32_t row0 = int32_t(blockIdx.x) * kRows, head0 = int32_t(blockIdx.y) * C::HEADS;
+  const bool is_v = (threadIdx.x / LANES) & 1;
+  const int lane = threadIdx.x % LANES, at = threadIdx.x / (2 * LANES);
+  const char* src = (is_v ? A.v : A.k) + lane * 16;
+  const int64_t st = is_v ? A.vs[0] : A.ks[0], sh_ = is_v ? A.vs[1] : A.ks[1];
+  src += (row0 + at) * st + head0 * sh_;
+  // the rows are asked for whatever their slots are: one latency, not two
+  uint4 raw[kPasses];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = 0.f;
-  if (there) {
-    const char* src = is_v ? A.v + t * A.vs[0] + head * A.vs[1] : A.k + t * A.ks[0] + head * A.ks[1];
-    const uint4 raw = *reinterpret_cast<const uint4*>(src + lane * 16);
-    const uint32_t* u = reinterpret_cast<const uint32_t*>(&raw);
+  for (int p = 0; p < kPasses; ++p) {
+    raw[p] = make_uint4(0, 0, 0, 0);
+    if (row0 + at + Piece<D>::row(p) < A.T && head0 + Piece<D>::head(p) < A.Hkv)
+      raw[p] = *reinterpret_cast<const uint4*>(src + Piece<D>::row(p) * st + Piece<D>::head(p) * sh_);
+  }
+  if (threadIdx.x < 32) {
+    int64_t tile = 0;
+    const int32_t slot = threadIdx.x < kRows ? find_slot(A, row0 + int(threadIdx.x), &tile) : -1;
+    const uint32_t key = uint32_t(slot & ~15) | uint32_t(Kv4Tile::v_pos(token_of(slot)));
+    int rank = 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const uint32_t other = __shfl_sync(0xffffffffu, key, i);
+      rank += other < key || (other == key && i < int(threadIdx.x));
+    }
+    if (threadIdx.x < kRows) {
+      s_slot[threadIdx.x] = slot;
+      s_tile[threadIdx.x] = tile;
+      s_order[rank] = int8_t(threadIdx.x);
+    }
+  }
+  __syncthreads();
+  auto tile_at = [&](int row, int hd) {
+    return A.cache + (s_tile[row] + int64_t(head0 + hd) * A.tpp) * L.bytes();
+  };
+
+#pragma unroll
+  for (int p = 0; p < kPasses; ++p) {
+    const int row = at + Piece<D>::row(p), hd = Piece<D>::head(p);
+    const int32_t slot = s_slot[row];
+    const bool there = slot >= 0 && head0 + hd < A.Hkv;
+    const uint32_t u[4] = {raw[p].x, raw[p].y, raw[p].z, raw[p].w};
+    float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (A.dtype == SPARGE_BF16) {
+      if (DT == SPARGE_BF16) {
         x[2 * i] = __uint_as_float(u[i] << 16);
         x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
       } else {
@@ -82,111 +147,161 @@ __global__ void __launch_bounds__(kCacheThreads) append_kernel(const CacheArgs A
         x[2 * i + 1] = f.y;
       }
     }
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(x[i]));
+#pragma unroll
+    for (int o = 1; o < GL; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // s = fp16(m / 7) and codes rint(x / s), the quotients correctly rounded by
+    // Markstein's step from a correctly rounded reciprocal y: q = q0 + (a - q0 b) y
+    // with q0 = a y.  (IEEE divisions took three times all other instructions.)
+    const bool high = m > 7.0f * kMaxScale;  // as m / 7 > kMaxScale: false for a NaN
+    if (high) {
+      m = 7.0f * kMaxScale;
+      if (there && A.status != nullptr) atomicCAS(A.status, 0, int32_t(SPARGE_ERANGE));
+    }
+    constexpr float kSeventh = 1.0f / 7.0f;
+    const float m0 = m * kSeventh;
+    const __half sh = __float2half_rn(fmaf(fmaf(-m0, 7.0f, m), kSeventh, m0));
+    const float s = __half2float(sh), most = 7.25f * s;
+    const float y = s > 0.f ? __frcp_rn(s) : 0.f;  // a scale of 0 or NaN has codes 0
+    // rounded to a whole number, plus 8, by the sum's own rounding: the low bits
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float z = fminf(fmaxf(x[i], -most), most);  // beyond it the code is 7 (inf too)
+      const float q0 = z * y;
+      const float q = fmaf(fmaf(-q0, s, z), y, q0);
+      c[i] = __float_as_uint((s > 0.f ? q : 0.f) + 12582920.0f) & 0xFFFFu;
+    }
+    if (!is_v) {
+      if (there) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) w += (c[e] | c[e + 1] << 16) << (2 * e);
+        *reinterpret_cast<uint32_t*>(tile_at(row, hd) + L.k_word(token_of(slot), lane % 4, lane / 4)) = w;
+      }
+    } else {
+      // channels 8 lane .. + 7 lie in block lane / 2: byte (lane / 2) % 4 of the
+      // words g = 4 (lane % 2) + 0..3
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        reinterpret_cast<uint8_t*>(&s_v[hd][8 * (lane / 8) + 4 * (lane % 2) + i][row])[lane / 2 % 4] =
+            uint8_t(c[2 * i] + (c[2 * i + 1] << 4));
+    }
+    if (lane % GL == 0) s_scale[hd][row][(is_v ? NG : 0) + lane / GL] = sh;
   }
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(x[i]));
-#pragma unroll
-  for (int o = 1; o < GL; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float sf = __fdiv_rn(m, 7.0f);
-  if (sf > kMaxScale) {  // false for a NaN
-    sf = kMaxScale;
-    if (there && A.status != nullptr) atomicCAS(A.status, 0, int32_t(SPARGE_ERANGE));
+  __syncthreads();
+
+  // ---- V's words in the order of their addresses, then the scales
+  for (int e = threadIdx.x; e < C::HEADS * WORDS * kRows; e += kCacheThreads) {
+    const int row = s_order[e % kRows], word = e / kRows % WORDS, hd = e / (kRows * WORDS);
+    const int32_t slot = s_slot[row];
+    if (slot < 0 || head0 + hd >= A.Hkv) continue;
+    *reinterpret_cast<uint32_t*>(tile_at(row, hd) + L.v_word(token_of(slot), word / 8, word % 8)) =
+        s_v[hd][word][row];
   }
-  const __half sh = __float2half_rn(sf);
-  const float s = __half2float(sh);
-  uint32_t c[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // a scale of 0 or NaN has codes 0
-    const float q = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -7.f), 7.f) : 0.f;
-    c[i] = uint32_t(int(q) + 8);
+  for (int e = threadIdx.x; e < C::HEADS * kRows * NG; e += kCacheThreads) {
+    const int n = e % NG, row = e / NG % kRows, hd = e / (NG * kRows);
+    const int32_t slot = s_slot[row];
+    if (slot < 0 || head0 + hd >= A.Hkv) continue;
+    reinterpret_cast<uint32_t*>(tile_at(row, hd) + L.k_scale(token_of(slot)))[n] =
+        reinterpret_cast<const uint32_t*>(s_scale[hd][row])[n];
   }
-  if (!there) return;
-  int tok;
-  uint8_t* tile = tile_of(A, slot, head, L.bytes(), &tok);
-  if (!is_v) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w |= c[e] << (4 * (e / 2) + 16 * (e % 2));
-    *reinterpret_cast<uint32_t*>(tile + L.k_word(tok, lane % 4, lane / 4)) = w;
-  } else {
-    // channels 8 lane .. + 7 of block lane / 2: g = 4 (lane % 2) + 0..3
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      tile[L.v_word(tok, lane / 8, 4 * (lane % 2) + i) + (lane / 2) % 4] =
-          uint8_t(c[2 * i] | (c[2 * i + 1] << 4));
-  }
-  if (lane % GL == 0)
-    reinterpret_cast<__half*>(tile + (is_v ? L.v_scale(tok) : L.k_scale(tok)))[lane / GL] = sh;
 }
 
-template <int D, int NG>
+template <int D, int NG, int DT>
 __global__ void __launch_bounds__(kCacheThreads) read_kernel(const CacheArgs A) {
-  constexpr int LANES = D / 8;
+  using C = CacheCfg<D>;
+  constexpr int LANES = C::LANES;
   constexpr int GL = D / NG / 8;
   constexpr Kv4Tile L{D, NG};
-  const int64_t thread = int64_t(blockIdx.x) * kCacheThreads + threadIdx.x;
-  const int64_t item = thread / (2 * LANES);
+  __shared__ int32_t s_slot[kRows];
+  __shared__ int64_t s_tile[kRows];
+  const int32_t row0 = int32_t(blockIdx.x) * kRows, head0 = int32_t(blockIdx.y) * C::HEADS;
   const bool is_v = (threadIdx.x / LANES) & 1;
-  const int lane = threadIdx.x % LANES;
-  if (item >= A.items) return;
-  const int32_t t = int32_t(item / A.Hkv), head = int32_t(item - int64_t(t) * A.Hkv);
-  const int32_t slot = A.slots[t];
-  const char* base = is_v ? A.v : A.k;
-  if (uint32_t(slot) >= uint32_t(A.slots_end) || base == nullptr) return;
-  int tok;
-  const uint8_t* tile = tile_of(A, slot, head, L.bytes(), &tok);
-  uint32_t c[8];
-  if (!is_v) {
-    const uint32_t w =
-        *reinterpret_cast<const uint32_t*>(tile + L.k_word(tok, lane % 4, lane / 4));
+  const int lane = threadIdx.x % LANES, at = threadIdx.x / (2 * LANES);
+  if (threadIdx.x < kRows) {
+    int64_t tile = 0;
+    s_slot[threadIdx.x] = find_slot(A, row0 + int(threadIdx.x), &tile);
+    s_tile[threadIdx.x] = tile;
+  }
+  __syncthreads();
+  constexpr int ES = DT == SPARGE_F32 ? 4 : 2;
+  char* dst = const_cast<char*>(is_v ? A.v : A.k);
+  const bool wanted = dst != nullptr;
+  const int64_t st = is_v ? A.vs[0] : A.ks[0], sh_ = is_v ? A.vs[1] : A.ks[1];
+  dst += (row0 + at) * st + head0 * sh_ + lane * 8 * ES;
+  // a lane's word: K's (t, j) of its own channels, V's word number `lane`
+  uint32_t word[kPasses];
+  __half sh[kPasses];
+  bool there[kPasses];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = (w >> (4 * (e / 2) + 16 * (e % 2))) & 15u;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t b = tile[L.v_word(tok, lane / 8, 4 * (lane % 2) + i) + (lane / 2) % 4];
-      c[2 * i] = b & 15u;
-      c[2 * i + 1] = b >> 4;
+  for (int p = 0; p < kPasses; ++p) {
+    const int row = at + Piece<D>::row(p), hd = Piece<D>::head(p);
+    const int32_t slot = s_slot[row];
+    there[p] = wanted && slot >= 0 && head0 + hd < A.Hkv;
+    word[p] = 0;
+    sh[p] = __ushort_as_half(0);
+    if (there[p]) {
+      const int tok = token_of(slot);
+      const uint8_t* tile = A.cache + (s_tile[row] + int64_t(head0 + hd) * A.tpp) * L.bytes();
+      word[p] = *reinterpret_cast<const uint32_t*>(
+          tile + (is_v ? L.v_word(tok, lane / 8, lane % 8) : L.k_word(tok, lane % 4, lane / 4)));
+      sh[p] = reinterpret_cast<const __half*>(
+          tile + (is_v ? L.v_scale(tok) : L.k_scale(tok)))[lane / GL];
     }
   }
-  const float s = __half2float(
-      reinterpret_cast<const __half*>(tile + (is_v ? L.v_scale(tok) : L.k_scale(tok)))[lane / GL]);
-  float x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = float(int(c[i]) - 8) * s;
-  const int64_t off = is_v ? t * A.vs[0] + head * A.vs[1] : t * A.ks[0] + head * A.ks[1];
-  char* dst = const_cast<char*>(base) + off + lane * (A.dtype == SPARGE_F32 ? 32 : 16);
-  if (A.dtype == SPARGE_F32) {
-    reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
-    uint4 r;
-    uint32_t* u = reinterpret_cast<uint32_t*>(&r);
+  for (int p = 0; p < kPasses; ++p) {
+    // the codes, eight halves of bytes at the low end of z: V's are byte
+    // (lane / 2) % 4 of the words 8 (lane / 8) + 4 (lane % 2) + 0..3, K's its word's
+    uint32_t z[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (A.dtype == SPARGE_BF16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t*>(&h);
-      } else {
-        const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t*>(&h);
-      }
+      const uint32_t w = __shfl_sync(0xffffffffu, word[p], 8 * (lane / 8) + 4 * (lane % 2) + i, LANES);
+      z[2 * i] = is_v ? w >> (8 * (lane / 2 % 4)) : word[p] >> (4 * i);
+      z[2 * i + 1] = is_v ? z[2 * i] >> 4 : z[2 * i] >> 16;
     }
-    *reinterpret_cast<uint4*>(dst) = r;
+    if (!there[p]) continue;
+    const float s = __half2float(sh[p]);
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)  // 2^23 + u, minus 2^23 + 8
+      x[i] = (__uint_as_float((z[i] & 15u) | 0x4B000000u) - 8388616.0f) * s;
+    char* to = dst + Piece<D>::row(p) * st + Piece<D>::head(p) * sh_;
+    if (DT == SPARGE_F32) {
+      reinterpret_cast<float4*>(to)[0] = make_float4(x[0], x[1], x[2], x[3]);
+      reinterpret_cast<float4*>(to)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+      uint32_t r[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (DT == SPARGE_BF16) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+          r[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+          r[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      *reinterpret_cast<uint4*>(to) = make_uint4(r[0], r[1], r[2], r[3]);
+    }
   }
 }
 
 template <bool READ, int D, int NG>
 cudaError_t run(const CacheArgs& a, cudaStream_t stream) {
-  const int64_t blocks = cdiv(a.items * (2 * D / 8), kCacheThreads);
-  if (blocks > INT32_MAX) return cudaErrorNotSupported;
-  if (READ)
-    read_kernel<D, NG><<<unsigned(blocks), kCacheThreads, 0, stream>>>(a);
-  else
-    append_kernel<D, NG><<<unsigned(blocks), kCacheThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  const dim3 grid(unsigned(cdiv(a.T, kRows)), unsigned(cdiv(a.Hkv, CacheCfg<D>::HEADS)));
+  const auto go = [&](auto* kernel) {
+    kernel<<<grid, kCacheThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+  };
+  if (a.dtype == SPARGE_F16)
+    return READ ? go(read_kernel<D, NG, SPARGE_F16>) : go(append_kernel<D, NG, SPARGE_F16>);
+  if (a.dtype == SPARGE_BF16)
+    return READ ? go(read_kernel<D, NG, SPARGE_BF16>) : go(append_kernel<D, NG, SPARGE_BF16>);
+  return READ ? go(read_kernel<D, NG, SPARGE_F32>) : cudaErrorNotSupported;
 }
 
 template <bool READ>
@@ -210,7 +325,7 @@ cudaError_t launch_kv4_cache(const sparge_kv4_t& c, bool read, int32_t T, void* 
   a.slots = slots;
   a.cache = static_cast<uint8_t*>(cache);
   a.status = status;
-  a.items = int64_t(T) * c.Hkv;
+  a.T = T;
   a.slots_end = c.num_pages * c.page_size;
   a.Hkv = c.Hkv;
   a.page = c.page_size;

@@ -26,40 +26,55 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanPer = 4;  // requests per thread
+constexpr int kRun = 8;      // tokens per thread and step
+constexpr int kBatch = 8;    // pages that come back, in flight per thread
 constexpr int kPlanMax = kPlanThreads * kPlanPer;
 static_assert(kPlanMax == kMaxPlanRequests, "every request has a thread");
 
-// Exclusive prefix sum of one value per thread; *total gets the sum.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sh, int64_t* total) {
+// Exclusive prefix sums of N values per thread, in place; total gets the sums.
+// sh: 32 values for each of the N.
+template <int N>
+__device__ __forceinline__ void block_scan(int64_t (&v)[N], int64_t* sh, int64_t (&total)[N]) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int64_t incl = v;
+  int64_t incl[N];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
+  for (int k = 0; k < N; ++k) {
+    incl[k] = v[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, incl[k], o);
+      if (lane >= o) incl[k] += up;
+    }
+    if (lane == 31) sh[32 * k + w] = incl[k];
   }
-  __syncthreads();  // sh may still be read from the last scan
-  if (lane == 31) sh[w] = incl;
   __syncthreads();
-  if (w == 0) {
-    int64_t s = sh[lane];
+  if (w < N) {
+    int64_t s = sh[32 * w + lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t up = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s += up;
     }
-    sh[lane] = s;
+    sh[32 * w + lane] = s;
   }
   __syncthreads();
-  *total = sh[31];
-  return (w > 0 ? sh[w - 1] : 0) + incl - v;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    total[k] = sh[32 * k + 31];
+    v[k] = (w > 0 ? sh[32 * k + w - 1] : 0) + incl[k] - v[k];
+  }
+}
+
+__device__ __forceinline__ int32_t pages_of(int32_t tokens, int32_t P) {
+  return int32_t((uint32_t(tokens) + uint32_t(P) - 1u) / uint32_t(P));
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs A) {
   namespace cg = cooperative_groups;
   const cg::cluster_group cluster = cg::this_cluster();
   const int rank = int(cluster.block_rank()), ctas = int(cluster.num_blocks());
-  __shared__ int64_t sh[32];
+  __shared__ int64_t sh1[64], sh2[32];
+  __shared__ unsigned long long s_popped;
   extern __shared__ int32_t s_dyn[];
   int32_t* s_cu = s_dyn;             // [R + 1] start of each request's tokens
   int32_t* s_len = s_cu + A.R + 1;   // [R] L; -1: no tokens or not admitted; -2 - L: ended
@@ -70,29 +85,33 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
   int64_t count = *A.free_count;
   count = count < 0 ? 0 : (count > A.num_pages ? A.num_pages : count);
 
-  // ---- lengths, what comes back, where tokens start
+  if (threadIdx.x == 0) s_popped = 0;
+
+  // ---- lengths, what comes back, where tokens start; `per` requests a thread
+  const int per = (A.R + kPlanThreads - 1) / kPlanThreads, first = threadIdx.x * per;
   int32_t L[kPlanPer], n[kPlanPer];
-  int64_t add = 0, back = 0;
+  int64_t sums[2] = {0, 0};  // tokens, pages that come back
 #pragma unroll
   for (int i = 0; i < kPlanPer; ++i) {
-    const int r = threadIdx.x * kPlanPer + i;
+    const int r = first + i;
     L[i] = n[i] = 0;
-    if (r < A.R) {
-      const int64_t l = A.seq_len[r];
-      L[i] = int32_t(l < 0 ? 0 : (l > cap ? cap : l));
+    if (i < per && r < A.R) {
+      const int32_t l = A.seq_len[r];
+      L[i] = l < 0 ? 0 : int32_t(l > cap ? cap : l);
       n[i] = A.new_len[r];
     }
-    if (n[i] > 0) add += n[i];
-    if (n[i] < 0) back += (L[i] + int64_t(P) - 1) / P;
+    if (n[i] > 0) sums[0] += n[i];
+    if (n[i] < 0) sums[1] += pages_of(L[i], P);
   }
-  int64_t tokens, pushed;
-  int64_t cu = block_scan(add, sh, &tokens);
-  int64_t put = block_scan(back, sh, &pushed);
-  int64_t avail = count + pushed;
+  int64_t totals[2];
+  block_scan(sums, sh1, totals);
+  int64_t cu = sums[0], put = sums[1];
+  const int64_t tokens = totals[0];
+  int64_t avail = count + totals[1];
   if (avail > A.num_pages) avail = A.num_pages;
 
   // ---- pages needed, admission
-  int64_t at = cu, need = 0;
+  int64_t at = cu, upto[1] = {0}, all[1];
   int32_t want[kPlanPer];
 #pragma unroll
   for (int i = 0; i < kPlanPer; ++i) {
@@ -101,21 +120,20 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
     if (n[i] > 0) {
       at += n[i];
       if (after <= cap && at <= A.max_tokens)
-        want[i] = int32_t((after + P - 1) / P - (int64_t(L[i]) + P - 1) / P);
+        want[i] = pages_of(int32_t(after), P) - pages_of(L[i], P);
     }
-    if (want[i] > 0) need += want[i];
+    if (want[i] > 0) upto[0] += want[i];
   }
-  int64_t all;
-  int64_t upto = block_scan(need, sh, &all);
-  int64_t taken = 0;
+  block_scan(upto, sh2, all);
+  int64_t popped = 0;  // pages that went up to this thread's last admitted request
 #pragma unroll
   for (int i = 0; i < kPlanPer; ++i) {
-    const int r = threadIdx.x * kPlanPer + i;
-    if (r >= A.R) break;
-    const int64_t before = upto;
-    if (want[i] > 0) upto += want[i];
-    const bool ok = want[i] == 0 || (want[i] > 0 && upto <= avail);
-    if (ok) taken += want[i];
+    const int r = first + i;
+    if (i >= per || r >= A.R) break;
+    const int64_t before = upto[0];
+    if (want[i] > 0) upto[0] += want[i];
+    const bool ok = want[i] == 0 || (want[i] > 0 && upto[0] <= avail);
+    if (ok && want[i] > 0) popped = upto[0];
     s_cu[r] = int32_t(cu > INT32_MAX ? INT32_MAX : cu);
     s_len[r] = ok ? L[i] : -1;
     const int64_t off = n[i] < 0 ? put : before;
@@ -123,19 +141,19 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
     if (n[i] > 0) cu += n[i];
     if (n[i] < 0) {
       s_len[r] = -2 - L[i];  // ended
-      put += (L[i] + int64_t(P) - 1) / P;
+      put += pages_of(L[i], P);
     }
   }
   if (threadIdx.x == 0) s_cu[A.R] = int32_t(tokens > INT32_MAX ? INT32_MAX : tokens);
-  int64_t popped;
-  block_scan(taken, sh, &popped);
+  // needs grow along the requests, so what is taken is the largest sum admitted
+  if (popped > 0) atomicMax(&s_popped, (unsigned long long)popped);
 
   cluster.sync();  // every CTA has read what the first one now overwrites
   if (rank == 0) {
 #pragma unroll
     for (int i = 0; i < kPlanPer; ++i) {
-      const int r = threadIdx.x * kPlanPer + i;
-      if (r >= A.R) break;
+      const int r = first + i;
+      if (i >= per || r >= A.R) break;
       const bool ok = s_len[r] >= 0;
       A.seq_len_out[r] = n[i] < 0 ? 0 : (ok ? L[i] + n[i] : L[i]);
       A.admitted[r] = ok || n[i] <= 0;
@@ -143,50 +161,100 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
     }
     if (threadIdx.x == 0) {
       A.cu_new[A.R] = s_cu[A.R];
-      *A.free_count_out = int32_t(avail - popped);
+      *A.free_count_out = int32_t(avail - int64_t(s_popped));
     }
     // pages of ended requests, a warp per request
     const int lane = threadIdx.x & 31;
     for (int r = threadIdx.x >> 5; r < A.R; r += kPlanThreads / 32) {
       if (s_len[r] > -2) continue;
-      const int pages = int((int64_t(-2 - s_len[r]) + P - 1) / P);
-      for (int j = lane; j < pages; j += 32) {
-        const int64_t to = count + s_off[r] + j;
-        if (to < A.num_pages) A.free_pages[to] = A.block_table[int64_t(r) * A.max_pages + j];
+      const int pages = pages_of(-2 - s_len[r], P);
+      const int32_t* row = A.block_table + int64_t(r) * A.max_pages;
+      int32_t* to = A.free_pages + count + s_off[r];
+      const int room = int(min(int64_t(pages), A.num_pages - count - s_off[r]));
+      for (int j0 = lane; j0 < room; j0 += 32 * kBatch) {
+        int32_t id[kBatch];  // loads first: one latency for all
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (j0 + 32 * k < room) id[k] = row[j0 + 32 * k];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (j0 + 32 * k < room) to[j0 + 32 * k] = id[k];
       }
     }
   }
   cluster.sync();  // the pushed pages are there
 
-  // ---- slots: one token per thread and step; the first token of a new page
-  // writes its table entry
+  // ---- slots: kRun consecutive tokens per thread and step, so that the search
+  // for the request is paid once for them; the first token of a new page writes
+  // its table entry
   const int32_t end = s_cu[A.R];
-  for (int64_t t = int64_t(rank) * kPlanThreads + threadIdx.x; t < A.max_tokens;
-       t += int64_t(ctas) * kPlanThreads) {
-    int32_t slot = -1;
-    if (t < end) {
-      int lo = 0, hi = A.R;  // the last request that starts at or before t
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_cu[mid] <= t) lo = mid; else hi = mid;
+  const int64_t runs = (int64_t(A.max_tokens) + kRun - 1) / kRun;
+  const bool vec = (reinterpret_cast<uintptr_t>(A.slot_map) & 15u) == 0;
+  for (int64_t n = int64_t(rank) * kPlanThreads + threadIdx.x; n < runs;
+       n += int64_t(ctas) * kPlanThreads) {
+    const int32_t t0 = int32_t(n * kRun);
+    int32_t slot[kRun];
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) slot[i] = -1;
+    if (t0 < end) {
+      int r = 0, hi = A.R;  // the last request that starts at or before t0
+      while (hi - r > 1) {
+        const int mid = (r + hi) >> 1;
+        if (s_cu[mid] <= t0) r = mid; else hi = mid;
       }
-      const int32_t len = s_len[lo];
-      if (len >= 0) {
-        const int64_t pos = int64_t(len) + (t - s_cu[lo]);
-        const int32_t page = int32_t(pos / P), in = int32_t(pos - int64_t(page) * P);
-        const int32_t have = int32_t((int64_t(len) + P - 1) / P);
-        int32_t* entry = A.block_table + int64_t(lo) * A.max_pages + page;
-        int32_t id;
-        if (page < have) {
-          id = *entry;
-        } else {
-          id = A.free_pages[avail - 1 - s_off[lo] - (page - have)];
-          if (in == 0) *entry = id;
+      // page p of request r, of which `have` pages were there before; its first
+      // token writes the table entry
+      auto page_id = [&](int r, int32_t p, int32_t have, bool write) {
+        int32_t* entry = A.block_table + int64_t(r) * A.max_pages + p;
+        if (p < have) return *entry;
+        const int32_t id = A.free_pages[avail - 1 - s_off[r] - (p - have)];
+        if (write) *entry = id;
+        return id;
+      };
+      const auto first_slot = [&](int32_t id) { return int32_t(uint32_t(id) * uint32_t(P)); };
+      if (t0 + kRun <= s_cu[r + 1] && P >= kRun) {
+        // all of one request and of one or two of its pages: nearly every run
+        const int32_t len = s_len[r];
+        if (len >= 0) {
+          const int32_t pos = len + (t0 - s_cu[r]), p = pos / P, have = pages_of(len, P);
+          const int32_t in = pos - p * P;
+          const int32_t a = first_slot(page_id(r, p, have, in == 0)) + in;
+          int32_t b = 0;  // so that b + i is token i's slot, if it is in the next page
+          if (in + kRun > P) b = first_slot(page_id(r, p + 1, have, true)) + in - P;
+#pragma unroll
+          for (int i = 0; i < kRun; ++i) slot[i] = (in + i < P ? a : b) + i;
         }
-        slot = int32_t(int64_t(id) * P + in);
+      } else {
+        int32_t next = s_cu[r + 1];    // where the request's tokens end
+        int32_t in = P, slot_at = -1;  // offset in the page at hand (P: none), next slot
+        for (int i = 0; i < kRun && t0 + i < end; ++i) {
+          const int32_t t = t0 + i;
+          while (t >= next) next = s_cu[++r + 1], in = P;
+          const int32_t len = s_len[r];
+          if (len < 0) continue;
+          if (in == P) {  // another page
+            const int32_t pos = len + (t - s_cu[r]), p = pos / P;
+            in = pos - p * P;
+            slot_at = first_slot(page_id(r, p, pages_of(len, P), in == 0)) + in;
+          }
+#pragma unroll
+          for (int k = 0; k < kRun; ++k)
+            if (k == i) slot[k] = slot_at;
+          ++slot_at;
+          ++in;
+        }
       }
     }
-    A.slot_map[t] = slot;
+    if (vec && t0 + kRun <= A.max_tokens) {
+#pragma unroll
+      for (int i = 0; i < kRun; i += 4)
+        *reinterpret_cast<int4*>(A.slot_map + t0 + i) =
+            make_int4(slot[i], slot[i + 1], slot[i + 2], slot[i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i)
+        if (t0 + i < A.max_tokens) A.slot_map[t0 + i] = slot[i];
+    }
   }
 }
 
@@ -194,10 +262,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
 
 cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  // up to eight CTAs (a portable cluster), one per 4096 tokens
-  const int64_t ctas = cdiv(a.max_tokens, 4 * kPlanThreads);
+  // a thread for kRun tokens, up to sixteen CTAs
+  const int64_t ctas = cdiv(a.max_tokens, int64_t(kRun) * kPlanThreads);
   int n = 1;
-  while (n < 8 && n < ctas) n <<= 1;
+  while (n < 16 && n < ctas) n <<= 1;
+  if (n > 8) {  // more than the portable cluster size
+    const cudaError_t e =
+        cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   cfg.gridDim = dim3(unsigned(n));
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = (3 * size_t(a.R) + 1) * sizeof(int32_t);
