@@ -8,8 +8,8 @@
 //
 // A CTA takes 16 rows of two (d = 128) or four heads, usually one tile of each,
 // at most parts of 16.  A row of d channels is held by d/8 lanes, eight channels
-// each, K's row by the lower half of 2 d/8 lanes and V's by the upper, and every
-// thread has four such pieces in flight.  K's codes of a token lie together and
+// each; every second warp takes V's rows, the others K's, and every thread has
+// four such pieces in flight.  K's codes of a token lie together and
 // are stored as they are; V's lie 64 bytes apart, next to those of the tile's
 // other tokens, so append gathers them in shared memory and stores them in the
 // cache's order, and read takes them as the words they are, from L1 after the
@@ -20,6 +20,7 @@
 #include <cstdint>
 
 #include "kv4_layout.cuh"
+#include "sm100_ptx.cuh"
 #include "sparge_internal.h"
 
 namespace sparge {
@@ -45,6 +46,7 @@ struct CacheArgs {
   int32_t* status;
   int32_t T, slots_end;  // slots_end: num_pages * page_size
   int32_t Hkv, page, tpp, dtype;  // tpp: tiles per page
+  uint32_t low4;  // 15; from a register, a mask and an or are one instruction
 };
 
 constexpr int kRows = 16;    // rows per CTA
@@ -95,8 +97,9 @@ __global__ void __launch_bounds__(kCacheThreads) append_kernel(const CacheArgs A
   __shared__ __align__(16) __half s_scale[C::HEADS][kRows][2 * NG];
 
   const int32_t row0 = int32_t(blockIdx.x) * kRows, head0 = int32_t(blockIdx.y) * C::HEADS;
-  const bool is_v = (threadIdx.x / LANES) & 1;
-  const int lane = threadIdx.x % LANES, at = threadIdx.x / (2 * LANES);
+  const bool is_v = threadIdx.x / 32 & 1;
+  const int lane = threadIdx.x % LANES;
+  const int at = threadIdx.x / 64 * (32 / LANES) + threadIdx.x % 32 / LANES;
   const char* src = (is_v ? A.v : A.k) + lane * 16;
   const int64_t st = is_v ? A.vs[0] : A.ks[0], sh_ = is_v ? A.vs[1] : A.ks[1];
   src += (row0 + at) * st + head0 * sh_;
@@ -163,31 +166,35 @@ __global__ void __launch_bounds__(kCacheThreads) append_kernel(const CacheArgs A
     constexpr float kSeventh = 1.0f / 7.0f;
     const float m0 = m * kSeventh;
     const __half sh = __float2half_rn(fmaf(fmaf(-m0, 7.0f, m), kSeventh, m0));
-    const float s = __half2float(sh), most = 7.25f * s;
-    const float y = s > 0.f ? __frcp_rn(s) : 0.f;  // a scale of 0 or NaN has codes 0
-    // rounded to a whole number, plus 8, by the sum's own rounding: the low bits
-    uint32_t c[8];
+    const float s = __half2float(sh);
+    // Codes pass 7 only where s was saturated or, below fp16's normal range, far
+    // from m / 7; a scale of 0 or NaN has codes 0.  Such groups clamp first.
+    if (high || !(s >= 6.103515625e-05f)) {
+      const float most = 7.25f * s;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float z = fminf(fmaxf(x[i], -most), most);  // beyond it the code is 7 (inf too)
-      const float q0 = z * y;
-      const float q = fmaf(fmaf(-q0, s, z), y, q0);
-      c[i] = __float_as_uint((s > 0.f ? q : 0.f) + 12582920.0f) & 0xFFFFu;
+      for (int i = 0; i < 8; ++i) x[i] = s > 0.f ? fminf(fmaxf(x[i], -most), most) : 0.f;
+    }
+    const float y = s > 0.f ? __frcp_rn(s) : 0.f;
+    const uint64_t y2 = pack2(y, y), s2 = pack2(s > 0.f ? -s : 0.f, s > 0.f ? -s : 0.f);
+    // rounded to a whole number, plus 8, by the sum's own rounding: the low bits
+    uint32_t c[4];  // two codes each, in the two half-words
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t z = pack2(x[2 * i], x[2 * i + 1]), q0 = mul2(z, y2);
+      const uint64_t q = add2(fma2(fma2(q0, s2, z), y2, q0), pack2(12582920.0f, 12582920.0f));
+      c[i] = __byte_perm(uint32_t(q), uint32_t(q >> 32), 0x5410);
     }
     if (!is_v) {
-      if (there) {
-        uint32_t w = 0;
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) w += (c[e] | c[e + 1] << 16) << (2 * e);
-        *reinterpret_cast<uint32_t*>(tile_at(row, hd) + L.k_word(token_of(slot), lane % 4, lane / 4)) = w;
-      }
+      if (there)
+        *reinterpret_cast<uint32_t*>(tile_at(row, hd) + L.k_word(token_of(slot), lane % 4, lane / 4)) =
+            c[0] + (c[1] << 4) + (c[2] << 8) + (c[3] << 12);
     } else {
       // channels 8 lane .. + 7 lie in block lane / 2: byte (lane / 2) % 4 of the
       // words g = 4 (lane % 2) + 0..3
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         reinterpret_cast<uint8_t*>(&s_v[hd][8 * (lane / 8) + 4 * (lane % 2) + i][row])[lane / 2 % 4] =
-            uint8_t(c[2 * i] + (c[2 * i + 1] << 4));
+            uint8_t(c[i] | (c[i] >> 12));
     }
     if (lane % GL == 0) s_scale[hd][row][(is_v ? NG : 0) + lane / GL] = sh;
   }
@@ -219,8 +226,9 @@ __global__ void __launch_bounds__(kCacheThreads) read_kernel(const CacheArgs A) 
   __shared__ int32_t s_slot[kRows];
   __shared__ int64_t s_tile[kRows];
   const int32_t row0 = int32_t(blockIdx.x) * kRows, head0 = int32_t(blockIdx.y) * C::HEADS;
-  const bool is_v = (threadIdx.x / LANES) & 1;
-  const int lane = threadIdx.x % LANES, at = threadIdx.x / (2 * LANES);
+  const bool is_v = threadIdx.x / 32 & 1;
+  const int lane = threadIdx.x % LANES;
+  const int at = threadIdx.x / 64 * (32 / LANES) + threadIdx.x % 32 / LANES;
   if (threadIdx.x < kRows) {
     int64_t tile = 0;
     s_slot[threadIdx.x] = find_slot(A, row0 + int(threadIdx.x), &tile);
@@ -254,21 +262,30 @@ __global__ void __launch_bounds__(kCacheThreads) read_kernel(const CacheArgs A) 
   }
 #pragma unroll
   for (int p = 0; p < kPasses; ++p) {
-    // the codes, eight halves of bytes at the low end of z: V's are byte
-    // (lane / 2) % 4 of the words 8 (lane / 8) + 4 (lane % 2) + 0..3, K's its word's
+    // the codes, at the low end of z: V's are the two halves of byte (lane / 2) % 4
+    // of the words 8 (lane / 8) + 4 (lane % 2) + 0..3, K's are all its word's
     uint32_t z[8];
+    if (is_v) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = __shfl_sync(0xffffffffu, word[p], 8 * (lane / 8) + 4 * (lane % 2) + i, LANES);
-      z[2 * i] = is_v ? w >> (8 * (lane / 2 % 4)) : word[p] >> (4 * i);
-      z[2 * i + 1] = is_v ? z[2 * i] >> 4 : z[2 * i] >> 16;
+      for (int i = 0; i < 4; ++i) {
+        z[2 * i] = __shfl_sync(0xffffffffu, word[p], 8 * (lane / 8) + 4 * (lane % 2) + i, LANES) >>
+                   (8 * (lane / 2 % 4));
+        z[2 * i + 1] = z[2 * i] >> 4;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[e] = word[p] >> (4 * (e / 2) + 16 * (e % 2));
     }
     if (!there[p]) continue;
     const float s = __half2float(sh[p]);
+    const uint64_t s2 = pack2(s, s);
     float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)  // 2^23 + u, minus 2^23 + 8
-      x[i] = (__uint_as_float((z[i] & 15u) | 0x4B000000u) - 8388616.0f) * s;
+    for (int i = 0; i < 8; i += 2) {  // 2^23 + u, minus 2^23 + 8
+      const uint64_t u = pack2(__uint_as_float((z[i] & A.low4) | 0x4B000000u),
+                               __uint_as_float((z[i + 1] & A.low4) | 0x4B000000u));
+      unpack2(mul2(add2(u, pack2(-8388616.0f, -8388616.0f)), s2), x[i], x[i + 1]);
+    }
     char* to = dst + Piece<D>::row(p) * st + Piece<D>::head(p) * sh_;
     if (DT == SPARGE_F32) {
       reinterpret_cast<float4*>(to)[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -331,6 +348,7 @@ cudaError_t launch_kv4_cache(const sparge_kv4_t& c, bool read, int32_t T, void* 
   a.page = c.page_size;
   a.tpp = c.page_size / 16;
   a.dtype = dtype;
+  a.low4 = 15;
   return read ? pick<true>(c, a, stream) : pick<false>(c, a, stream);
 }
 
