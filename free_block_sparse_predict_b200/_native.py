@@ -53,14 +53,12 @@ class SpargeKv4Attn(ctypes.Structure):
                 ("q_stride", ctypes.c_int64)]
 
 
+# Parameter structs that go in as packed bytes or by reference are plain pointers here.
 _P = ctypes.POINTER(SpargeParams)
-_A = ctypes.POINTER(SpargeKv4Attn)
 _K = ctypes.POINTER(SpargeKv4)
-_R = ctypes.POINTER(SpargeRope)
 _V = ctypes.c_void_p
 _I = ctypes.c_int32
 _S = ctypes.c_size_t
-_D = ctypes.POINTER(ctypes.c_int64)
 
 SIGNATURES = {
     "sparge_workspace_bytes": (_S, [_P]),
@@ -74,14 +72,14 @@ SIGNATURES = {
     "sparge_predict_select": (ctypes.c_int, [_P, _V, _V, _V, _V, _V, _V, _S, _V]),
     "sparge_mask_compact": (ctypes.c_int, [_P, _V, _V, _V, _V]),
     "sparge_attn_fwd": (ctypes.c_int, [_P, _V, _V, _V, _V, _V, _V, _V, _S, _V, _V]),
-    "sparge_rope_apply": (ctypes.c_int, [_R, _V, _V, _V, _V, _V, _V, _V]),
-    "sparge_rope_inverse": (ctypes.c_int, [_R, _V, _V, _V, _V, _V, _V, _V]),
+    "sparge_rope_apply": (ctypes.c_int, [_V, _V, _V, _V, _V, _V, _V, _V]),
+    "sparge_rope_inverse": (ctypes.c_int, [_V, _V, _V, _V, _V, _V, _V, _V]),
     "sparge_kv_plan": (ctypes.c_int, [_I] * 5 + [_V] * 11),
     "sparge_kv4_bytes": (_S, [_K]),
-    "sparge_kv4_append": (ctypes.c_int, [_K, _I, _V, _D, _V, _D, ctypes.c_int, _V, _V, _V, _V]),
-    "sparge_kv4_read": (ctypes.c_int, [_K, _I, _V, _V, _V, _D, _V, _D, ctypes.c_int, _V]),
-    "sparge_kv4_workspace_bytes": (_S, [_K, _A]),
-    "sparge_kv4_attn": (ctypes.c_int, [_K, _A, _V, _V, _V, _V, _V, _V, _V, _V, _S, _V]),
+    "sparge_kv4_append": (ctypes.c_int, [_K, _I, _V, _V, _V, _V, ctypes.c_int, _V, _V, _V, _V]),
+    "sparge_kv4_read": (ctypes.c_int, [_K, _I, _V, _V, _V, _V, _V, _V, ctypes.c_int, _V]),
+    "sparge_kv4_workspace_bytes": (_S, [_K, _V]),
+    "sparge_kv4_attn": (ctypes.c_int, [_K, _V, _V, _V, _V, _V, _V, _V, _V, _V, _S, _V]),
     "sparge_device_status": (ctypes.c_int, [_V, _V]),
     "sparge_selftest_wait_timeout": (ctypes.c_int, [_V, _V]),
     "sparge_status_string": (ctypes.c_char_p, [ctypes.c_int]),

@@ -9,7 +9,7 @@ device that owns its tensors, on that device's current stream unless one is give
 from __future__ import annotations
 
 import ctypes
-import math
+import struct
 from typing import NamedTuple, Optional
 
 import torch
@@ -23,40 +23,50 @@ __all__ = ["Rope", "rope_frequencies", "grid_positions", "sparge_rope_apply",
            "sparge_kv4_workspace_bytes", "kv4_workspace", "sparge_kv4_attn"]
 
 _DT = {torch.float16: SPARGE_F16, torch.bfloat16: SPARGE_BF16, torch.float32: SPARGE_F32}
+_I32, _F32, _F64, _U8 = torch.int32, torch.float32, torch.float64, torch.uint8
+
+# A single token's kernels run for microseconds, so these functions stay short: parameter
+# structs are packed in one step (the C layout of SpargeRope and SpargeKv4Attn), tensors are
+# checked by the cheapest accessors.
+_ROPE = struct.Struct("@8i7q")
+_ATTN = struct.Struct("@7ifiq")
+assert _ROPE.size == ctypes.sizeof(SpargeRope) and _ATTN.size == ctypes.sizeof(SpargeKv4Attn)
 
 
 def _bad(msg: str) -> SpargeError:
     return SpargeError(1, msg)
 
 
-def _check(code: int) -> None:
-    if code != 0:
-        raise SpargeError(code, lib().sparge_status_string(code).decode())
+def _raise(code: int) -> None:
+    raise SpargeError(code, lib().sparge_status_string(code).decode())
 
 
-def _stream(stream, device) -> int:
+def _stream(stream, device: int) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        return torch._C._cuda_getCurrentRawStream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _device(t: torch.Tensor, name: str):
-    if not t.is_cuda:
+def _device(t: torch.Tensor, name: str) -> int:
+    """Number of the CUDA device that owns t."""
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
         raise _bad(f"{name}: expected a CUDA tensor")
-    return t.device
+    return dev
 
 
-def _flat(t, name: str, numel: int, dtype, device) -> int:
-    """Address of a contiguous tensor of at least numel elements of dtype on device."""
-    if t.device != device:
-        raise _bad(f"{name}: expected a tensor on {device}, got {t.device}")
-    if t.dtype != dtype:
+def _flat(t, name: str, numel: int, dtype, device: int) -> int:
+    """Address of a contiguous tensor of at least numel elements of dtype on the device."""
+    if (t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+            and t.numel() >= numel):
+        return t.data_ptr()
+    if t.get_device() != device:
+        raise _bad(f"{name}: expected a tensor on cuda:{device}, got {t.device}")
+    if t.dtype is not dtype:
         raise _bad(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise _bad(f"{name}: expected a contiguous tensor")
-    if t.numel() < numel:
-        raise _bad(f"{name}: needs {numel} elements, has {t.numel()}")
-    return t.data_ptr()
+    raise _bad(f"{name}: needs {numel} elements, has {t.numel()}")
 
 
 # ----------------------------------------------------------------------------
@@ -104,32 +114,39 @@ def grid_positions(N: int, prefix_len: int, T: int, Hg: int, Wg: int, device="cu
 
 def _rope(inverse, x, y, pos, inv_freq, axis, perm, interleaved, stream):
     dev = _device(x, "x")
-    if x.dim() != 4 or x.shape != y.shape or x.dtype != y.dtype or x.dtype not in _DT:
+    shape, dtype = x.shape, x.dtype
+    code = _DT.get(dtype)
+    if len(shape) != 4 or shape != y.shape or y.dtype is not dtype or code is None:
         raise _bad("expected two [B, H, N, d] tensors of one shape and floating dtype")
-    if y.device != dev:
-        raise _bad(f"y: expected a tensor on {dev}, got {y.device}")
-    B, H, N, d = x.shape
-    sx, sy = x.stride(), y.stride()
-    if d > 1 and (sx[3] != 1 or sy[3] != 1):
+    if y.get_device() != dev:
+        raise _bad(f"y: expected a tensor on cuda:{dev}, got {y.device}")
+    B, H, N, d = shape
+    xb, xh, xn, xd = x.stride()
+    yb, yh, yn, yd = y.stride()
+    if d > 1 and (xd != 1 or yd != 1):
         raise _bad("the channels have to be contiguous")
-    if pos.dim() not in (2, 3) or pos.shape[-1] != N or (pos.dim() == 3 and pos.shape[0] != B):
+    ps, pst = pos.shape, pos.stride()
+    if len(ps) not in (2, 3) or ps[-1] != N or (len(ps) == 3 and ps[0] != B):
         raise _bad("pos: expected [axes, N] or [B, axes, N]")
-    if pos.dtype != torch.int32 or pos.device != dev:
-        raise _bad(f"pos: expected {torch.int32} on {dev}")
-    axes, sp = pos.shape[-2], pos.stride()
-    if (N > 1 and sp[-1] != 1) or (axes > 1 and sp[-2] != N):
+    if pos.dtype is not _I32 or pos.get_device() != dev:
+        raise _bad(f"pos: expected torch.int32 on cuda:{dev}")
+    axes = ps[-2]
+    if (N > 1 and pst[-1] != 1) or (axes > 1 and pst[-2] != N):
         raise _bad("pos: expected contiguous [axes, N] rows")
     pairs = inv_freq.numel()
-    p = SpargeRope(B, H, N, d, 2 * pairs, axes, int(interleaved), _DT[x.dtype],
-                   (sx[0], sx[1], sx[2]), (sy[0], sy[1], sy[2]), sp[0] if pos.dim() == 3 else 0)
-    args = (pos.data_ptr(), _flat(inv_freq, "inv_freq", pairs, torch.float64, dev),
-            _flat(axis, "axis", pairs, torch.int32, dev),
-            None if perm is None else _flat(perm, "perm", N, torch.int32, dev),
-            _stream(stream, dev))
+    p = _ROPE.pack(B, H, N, d, 2 * pairs, axes, 1 if interleaved else 0, code, xb, xh, xn,
+                   yb, yh, yn, pst[0] if len(ps) == 3 else 0)
+    f = _flat(inv_freq, "inv_freq", pairs, _F64, dev)
+    ax = _flat(axis, "axis", pairs, _I32, dev)
+    table = None if perm is None else _flat(perm, "perm", N, _I32, dev)
     if inverse:
-        _check(lib().sparge_rope_inverse(ctypes.byref(p), y.data_ptr(), x.data_ptr(), *args))
+        rc = lib().sparge_rope_inverse(p, y.data_ptr(), x.data_ptr(), pos.data_ptr(), f, ax, table,
+                                       _stream(stream, dev))
     else:
-        _check(lib().sparge_rope_apply(ctypes.byref(p), x.data_ptr(), y.data_ptr(), *args))
+        rc = lib().sparge_rope_apply(p, x.data_ptr(), y.data_ptr(), pos.data_ptr(), f, ax, table,
+                                     _stream(stream, dev))
+    if rc:
+        _raise(rc)
 
 
 def sparge_rope_apply(x, y, pos, inv_freq, axis, perm: Optional[torch.Tensor] = None,
@@ -161,16 +178,18 @@ def sparge_kv_plan(new_len, seq_len, block_table, free_pages, free_count, page_s
     dev = _device(cu_new, "cu_new")
     if block_table.dim() != 2:
         raise _bad("block_table: expected [R, max_pages]")
-    (R, width), i32 = block_table.shape, torch.int32
-    pages, tokens = free_pages.numel(), slot_map.numel()
-    _check(lib().sparge_kv_plan(
-        R, page_size, width, pages, tokens, _flat(new_len, "new_len", R, i32, dev),
-        _flat(seq_len, "seq_len", R, i32, dev), _flat(block_table, "block_table", 0, i32, dev),
-        _flat(free_pages, "free_pages", 0, i32, dev), _flat(free_count, "free_count", 1, i32, dev),
-        _flat(seq_len_out, "seq_len_out", R, i32, dev),
-        _flat(free_count_out, "free_count_out", 1, i32, dev),
-        _flat(cu_new, "cu_new", R + 1, i32, dev), _flat(slot_map, "slot_map", 0, i32, dev),
-        _flat(admitted, "admitted", R, i32, dev), _stream(stream, dev)))
+    R, width = block_table.shape
+    rc = lib().sparge_kv_plan(
+        R, page_size, width, free_pages.numel(), slot_map.numel(),
+        _flat(new_len, "new_len", R, _I32, dev), _flat(seq_len, "seq_len", R, _I32, dev),
+        _flat(block_table, "block_table", 0, _I32, dev),
+        _flat(free_pages, "free_pages", 0, _I32, dev), _flat(free_count, "free_count", 1, _I32, dev),
+        _flat(seq_len_out, "seq_len_out", R, _I32, dev),
+        _flat(free_count_out, "free_count_out", 1, _I32, dev),
+        _flat(cu_new, "cu_new", R + 1, _I32, dev), _flat(slot_map, "slot_map", 0, _I32, dev),
+        _flat(admitted, "admitted", R, _I32, dev), _stream(stream, dev))
+    if rc:
+        _raise(rc)
 
 
 # ----------------------------------------------------------------------------
@@ -195,29 +214,29 @@ def kv4_cache(c: SpargeKv4, device="cuda") -> torch.Tensor:
                        device=device)
 
 
-_I64x2 = ctypes.c_int64 * 2
+_PAIR = struct.Struct("@2q").pack
 
 
-def _rows(x, name, c, T, dev, dtypes):
-    """Address and token / head strides of a [T, Hkv, d] tensor."""
-    if x.device != dev:
-        raise _bad(f"{name}: expected a tensor on {dev}, got {x.device}")
-    if x.dim() != 3 or tuple(x.shape) != (T, c.Hkv, c.d):
-        raise _bad(f"{name}: expected [{T}, {c.Hkv}, {c.d}], got {list(x.shape)}")
-    if x.dtype not in dtypes:
-        raise _bad(f"{name}: got {x.dtype}")
-    s = x.stride()
-    if s[2] != 1:
+def _rows(x, name, T, Hkv, d, dev):
+    """Address and packed token / head strides of a [T, Hkv, d] tensor."""
+    if x.get_device() != dev:
+        raise _bad(f"{name}: expected a tensor on cuda:{dev}, got {x.device}")
+    if x.shape != (T, Hkv, d):
+        raise _bad(f"{name}: expected [{T}, {Hkv}, {d}], got {list(x.shape)}")
+    st, sh, sd = x.stride()
+    if sd != 1:
         raise _bad(f"{name}: the channels have to be contiguous")
-    return x.data_ptr(), _I64x2(s[0], s[1])
+    return x.data_ptr(), _PAIR(st, sh)
 
 
-def _cache_ptr(c, cache) -> int:
-    need = sparge_kv4_bytes(c)
-    if need == 0 and c.num_pages != 0:
+def _cache_ptr(c, cache, Hkv: int, d: int, dev: int) -> int:
+    group = c.group
+    if group <= 0:
         raise _bad("invalid cache parameters")
-    if cache.dtype != torch.uint8 or not cache.is_contiguous() or cache.numel() < need:
-        raise _bad(f"cache: expected {need} contiguous bytes")
+    need = c.num_pages * Hkv * c.page_size * (d + 4 * (d // group))
+    if (cache.dtype is not _U8 or not cache.is_contiguous() or cache.numel() < need
+            or cache.get_device() != dev):
+        raise _bad(f"cache: expected {need} contiguous bytes on cuda:{dev}")
     return cache.data_ptr()
 
 
@@ -225,35 +244,43 @@ def sparge_kv4_append(c: SpargeKv4, k, v, slot_map, cache, status=None, stream=N
     """Rows of k and v [T, Hkv, d] (any token and head strides) into the slots slot_map [T];
     slots outside the cache are skipped.  status: an int32 tensor, or a workspace, whose first
     word receives SPARGE_ERANGE (6) when a scale was saturated."""
-    dev, T = _device(cache, "cache"), slot_map.numel()
-    pc = _cache_ptr(c, cache)
-    pk, sk = _rows(k, "k", c, T, dev, (torch.float16, torch.bfloat16))
-    pv, sv = _rows(v, "v", c, T, dev, (k.dtype,))
+    dev, T, Hkv, d = _device(cache, "cache"), slot_map.numel(), c.Hkv, c.d
+    dtype = k.dtype
+    if dtype not in _DT or v.dtype is not dtype:
+        raise _bad(f"k, v: expected one floating dtype, got {dtype} and {v.dtype}")
+    pk, sk = _rows(k, "k", T, Hkv, d, dev)
+    pv, sv = _rows(v, "v", T, Hkv, d, dev)
     if status is not None:
-        if status.device != dev or status.numel() * status.element_size() < 4:
-            raise _bad(f"status: expected 4 bytes on {dev}")
+        if status.get_device() != dev or status.numel() * status.element_size() < 4:
+            raise _bad(f"status: expected 4 bytes on cuda:{dev}")
         status = status.data_ptr()
-    _check(lib().sparge_kv4_append(ctypes.byref(c), T, pk, sk, pv, sv, _DT[k.dtype],
-                                   _flat(slot_map, "slot_map", T, torch.int32, dev), pc, status,
-                                   _stream(stream, dev)))
+    rc = lib().sparge_kv4_append(ctypes.byref(c), T, pk, sk, pv, sv, _DT[dtype],
+                                 _flat(slot_map, "slot_map", T, _I32, dev),
+                                 _cache_ptr(c, cache, Hkv, d, dev), status, _stream(stream, dev))
+    if rc:
+        _raise(rc)
 
 
 def sparge_kv4_read(c: SpargeKv4, cache, slot_map, k, v, stream=None) -> None:
     """The values that the slots slot_map [T] hold, into rows of k and v [T, Hkv, d] (16-bit or
     float32; either may be None); rows whose slot is outside the cache stay as they were."""
-    dev, T = _device(cache, "cache"), slot_map.numel()
-    pc = _cache_ptr(c, cache)
+    dev, T, Hkv, d = _device(cache, "cache"), slot_map.numel(), c.Hkv, c.d
     pk = pv = sk = sv = None
     first = k if k is not None else v
     if first is None:
         return
+    dtype = first.dtype
+    if dtype not in _DT or (v is not None and v.dtype is not dtype):
+        raise _bad("k, v: expected one floating dtype")
     if k is not None:
-        pk, sk = _rows(k, "k", c, T, dev, _DT)
+        pk, sk = _rows(k, "k", T, Hkv, d, dev)
     if v is not None:
-        pv, sv = _rows(v, "v", c, T, dev, (first.dtype,) if first.dtype in _DT else ())
-    _check(lib().sparge_kv4_read(ctypes.byref(c), T, pc,
-                                 _flat(slot_map, "slot_map", T, torch.int32, dev), pk, sk, pv, sv,
-                                 _DT[first.dtype], _stream(stream, dev)))
+        pv, sv = _rows(v, "v", T, Hkv, d, dev)
+    rc = lib().sparge_kv4_read(ctypes.byref(c), T, _cache_ptr(c, cache, Hkv, d, dev),
+                               _flat(slot_map, "slot_map", T, _I32, dev), pk, sk, pv, sv,
+                               _DT[dtype], _stream(stream, dev))
+    if rc:
+        _raise(rc)
 
 
 # ----------------------------------------------------------------------------
@@ -286,25 +313,27 @@ def sparge_kv4_attn(c: SpargeKv4, q, cache, block_table, seq_len, cu_q, max_q: i
     [R, max_pages], seq_len [R] and cu_q [R + 1] as sparge_kv_plan leaves them; max_q: most new
     tokens of a request; max_len: longest request (0: what the table holds); scale: 1/sqrt(d)
     unless given."""
-    dev = _device(q, "q")
-    if q.dim() != 3 or q.dtype not in (torch.float16, torch.bfloat16) or q.shape[2] != c.d:
-        raise _bad(f"q: expected [T, Hq, {c.d}] in 16 bits")
-    T, Hq, d = q.shape
-    sq = q.stride()
-    if sq[2] != 1 or (Hq > 1 and sq[1] != d):
+    dev, shape, dtype, d = _device(q, "q"), q.shape, q.dtype, c.d
+    if len(shape) != 3 or shape[2] != d or dtype not in _DT or dtype is _F32:
+        raise _bad(f"q: expected [T, Hq, {d}] in 16 bits")
+    T, Hq, _ = shape
+    st, sh, sd = q.stride()
+    if sd != 1 or (Hq > 1 and sh != d):
         raise _bad("q: heads and channels have to be contiguous")
-    if o.shape != q.shape:
-        raise _bad(f"o: expected {list(q.shape)}")
+    if o.shape != shape:
+        raise _bad(f"o: expected {list(shape)}")
     if block_table.dim() != 2:
         raise _bad("block_table: expected [R, max_pages]")
-    (R, width), i32 = block_table.shape, torch.int32
-    if cache.device != dev or ws.device != dev or not ws.is_contiguous():
-        raise _bad(f"cache, ws: expected contiguous tensors on {dev}")
-    a = SpargeKv4Attn(R, T, Hq, max_q, width, max_len, int(causal),
-                      1.0 / math.sqrt(d) if scale is None else scale, _DT[q.dtype], sq[0])
-    _check(lib().sparge_kv4_attn(
-        ctypes.byref(c), ctypes.byref(a), q.data_ptr(), _cache_ptr(c, cache),
-        _flat(block_table, "block_table", 0, i32, dev), _flat(seq_len, "seq_len", R, i32, dev),
-        _flat(cu_q, "cu_q", R + 1, i32, dev), _flat(o, "o", 0, q.dtype, dev),
-        None if lse is None else _flat(lse, "lse", T * Hq, torch.float32, dev), ws.data_ptr(),
-        ws.numel() * ws.element_size(), _stream(stream, dev)))
+    R, width = block_table.shape
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise _bad(f"ws: expected a contiguous tensor on cuda:{dev}")
+    a = _ATTN.pack(R, T, Hq, max_q, width, max_len, 1 if causal else 0,
+                   d ** -0.5 if scale is None else scale, _DT[dtype], st)
+    rc = lib().sparge_kv4_attn(
+        ctypes.byref(c), a, q.data_ptr(), _cache_ptr(c, cache, c.Hkv, d, dev),
+        _flat(block_table, "block_table", 0, _I32, dev), _flat(seq_len, "seq_len", R, _I32, dev),
+        _flat(cu_q, "cu_q", R + 1, _I32, dev), _flat(o, "o", 0, dtype, dev),
+        None if lse is None else _flat(lse, "lse", T * Hq, _F32, dev), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _stream(stream, dev))
+    if rc:
+        _raise(rc)
