@@ -42,69 +42,20 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "kv4_common.cuh"
 #include "kv4_layout.cuh"
 #include "sm100_ptx.cuh"
 #include "sparge_internal.h"
 
 namespace sparge {
+
+using namespace kv4;
+
 namespace {
 
-constexpr int kSms = 148;
 constexpr int kWarps = 4;
 constexpr int kAttnThreads = kWarps * 32;
-constexpr float kLow = -1e30f;     // "no key yet"; finite, so differences stay numbers
 constexpr float kLazy = 2.0f;      // log2 units
-
-// Division by a number that the host knows: n / d = umulhi(n, mul) >> shift
-// for n < 2^31 (Granlund and Montgomery's round-up method, 32 + 1 bits of
-// precision for a 31-bit numerator).
-struct Div {
-  uint32_t d, mul, shift;
-  __device__ __forceinline__ int32_t quot(int32_t n) const {
-    return d == 1 ? n : int32_t(__umulhi(uint32_t(n), mul) >> shift);
-  }
-};
-Div make_div(uint32_t d) {
-  Div x{d, 0, 0};
-  if (d > 1) {
-    uint32_t log = 0;
-    while ((uint64_t(1) << log) < d) ++log;  // ceil(log2 d)
-    x.shift = log - 1;
-    x.mul = uint32_t(((uint64_t(1) << (31 + log)) + d - 1) / d);
-  }
-  return x;
-}
-
-struct Masks {
-  uint32_t low, high;  // 0x000F000F, 0x00F000F0
-};
-struct DecodeArgs {
-  const char* q;
-  const uint8_t* cache;
-  const int32_t* table;
-  const int32_t* seq_len;
-  const int32_t* cu;
-  char* o;
-  float* lse;
-  float* part_o;      // [2 C][8 NT][d]: a CTA's first and last unit
-  float2* part_ml;    // [2 C][8 NT]: maximum (log2) and sum
-  uint32_t* arrived;  // [C]: parts of the unit that starts in CTA c; 0 between calls
-  int32_t* status;
-  int64_t q_stride;  // bytes
-  int32_t R, T, Hq, Hkv, max_q, max_pages, len_cap, causal, num_pages, bf16;
-  Div G, heads, tpp;  // query heads per KV head, KV heads, tiles per page
-  Masks masks;
-  float scale_log2;
-};
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -119,55 +70,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
-// The codes at bits 0-3 and 4-7 of both half-words, as fp16 pairs.
-__device__ __forceinline__ uint32_t minus(uint32_t x, uint32_t y) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(y));
-  return d;
-}
-__device__ __forceinline__ uint32_t times(uint32_t x, uint32_t y) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(y));
-  return d;
-}
-// (w & mask) | magic; a LOP3 takes one immediate, so the mask is in a register
-// whose value the compiler does not know (it would make two instructions of it)
-__device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t mask, uint32_t magic) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
-  return d;
-}
-__device__ __forceinline__ uint32_t codes0(uint32_t w, const Masks& k) {
-  return minus(pick(w, k.low, 0x64006400u), 0x64086408u);  // 1024 + u, 1032
-}
-__device__ __forceinline__ uint32_t codes4(uint32_t w, const Masks& k) {
-  return minus(pick(w, k.high, 0x54005400u), 0x54805480u);  // 64 + u, 72
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
-}
-
-__device__ __forceinline__ float2 half2_f(uint32_t u) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&u));
-}
-
-// Request r's rows and keys, as every kernel here takes them.
-struct Request {
-  int32_t q0, qlen, len, keys;  // first row, rows, length, keys in reach
-  bool sound;
-};
-__device__ __forceinline__ Request request(const DecodeArgs& A, int r) {
-  Request x;
-  x.q0 = A.cu[r];
-  const int32_t q1 = A.cu[r + 1];
-  x.len = A.seq_len[r];
-  x.sound = x.q0 >= 0 && q1 >= x.q0 && q1 <= A.T && q1 - x.q0 <= A.max_q;
-  x.qlen = x.sound ? q1 - x.q0 : 0;
-  if (x.len < 0 || x.len > A.len_cap) x.sound = false;
-  x.keys = x.len < 0 ? 0 : (x.len > A.len_cap ? A.len_cap : x.len);
-  return x;
 }
 
 // A unit's start and end cost a CTA about as much as this many keys: the
@@ -175,22 +81,6 @@ __device__ __forceinline__ Request request(const DecodeArgs& A, int r) {
 // keys with every SM full).  Without it, many short requests met one CTA: nine
 // requests of 4001 to 1 tokens took 45 us, with it 15.
 constexpr int kUnitKeys = 256;
-
-// Length of request r's units in steps of KEYS keys (a unit without keys still
-// has its rows to write), and how many there are.
-template <int KEYS>
-__device__ __forceinline__ int64_t unit_steps(const Request& x) {
-  return x.keys > 0 ? (int64_t(x.keys) + KEYS - 1) / KEYS : 1;
-}
-template <int ROWS>
-__device__ __forceinline__ int64_t unit_count(const DecodeArgs& A, const Request& x) {
-  return int64_t(A.Hkv) * ((int64_t(x.qlen) * A.G.d + ROWS - 1) / ROWS);
-}
-
-// a / b, in 32 bits where both fit.
-__device__ __forceinline__ int64_t div64(int64_t a, int64_t b) {
-  return (a | b) >> 32 ? a / b : int64_t(uint32_t(a) / uint32_t(b));
-}
 
 // Resident CTAs per SM, by registers (128 and 255 a thread).
 __host__ __device__ constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : 2; }
@@ -243,28 +133,6 @@ __device__ __forceinline__ void load_scales_twice(const uint8_t* at, uint32_t (&
     const uint32_t w = *reinterpret_cast<const uint16_t*>(at);
     x[0] = __byte_perm(w, w, 0x1010);
   }
-}
-
-// Row `row` (query token times head of the group) of a request and KV head in q and o.
-__device__ __forceinline__ int64_t out_row(const DecodeArgs& A, const Request& x, int kvh, int row) {
-  const int tok = A.G.quot(row);
-  return int64_t(x.q0 + tok) * A.Hq + kvh * int(A.G.d) + (row - tok * int(A.G.d));
-}
-
-// One row's final value pair and, from the thread of its first channel, lse.
-__device__ __forceinline__ void write_out(const DecodeArgs& A, int64_t at, int D, int ch, float top,
-                                          float sum, float x, float y) {
-  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-  if (sum == 0.f) x = y = 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(A.o) + (at * D + ch) / 2;
-  if (A.bf16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x * inv, y * inv);
-    *dst = *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    *dst = pack_half2(x * inv, y * inv);
-  }
-  if (ch == 0 && A.lse != nullptr)
-    A.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <int D, int NG, int NT>
@@ -856,32 +724,50 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
 }
 
 struct Plan {
-  int32_t nt, grid;
+  int32_t nt, grid;   // column tiles and CTAs of the kernel above
+  int32_t piece_grid;  // CTAs of the other, 0: not needed
 };
+
+// More rows than this per request and KV head (tokens times the group's heads)
+// are a piece of a prompt, kv4_piece.cu: there a key costs a SM 10 to 20 clocks
+// for up to 256 rows, here some 10 for every 16.
+constexpr int64_t kFewRows = 32;
 
 // CTAs from the bounds that the host knows (lengths are on the device): all
 // that are resident at once, fewer when there cannot be a step for each warp.
-Plan make_plan(const sparge_kv4_t& c, const sparge_kv4_attn_t& a) {
-  Plan p{};
-  const int64_t rows = int64_t(a.max_q) * (a.Hq / c.Hkv);
-  p.nt = rows <= 8 ? 1 : 2;
-  const int64_t steps = cdiv(kv4_len_cap(c, a), 32);
-  const int64_t most = kSms * ctas_per_sm(p.nt);
+int32_t grid_of(const sparge_kv4_t& c, const sparge_kv4_attn_t& a, int64_t tiles, int64_t keys,
+                int64_t most, int64_t per_cta) {
+  const int64_t steps = cdiv(kv4_len_cap(c, a), keys);
   // more than that many CTAs' steps already: no need to multiply on
   int64_t line = steps < 1 ? 1 : steps;
-  const int64_t by[] = {cdiv(rows, 8 * p.nt), c.Hkv, a.R};
-  for (int64_t n : by) line = line > most * kWarps ? line : line * (n < 1 ? 1 : n);
-  const int64_t grid = cdiv(line, kWarps);
-  p.grid = int32_t(grid < most ? grid : most);
+  const int64_t by[] = {tiles, c.Hkv, a.R};
+  for (int64_t n : by) line = line > most * per_cta ? line : line * (n < 1 ? 1 : n);
+  const int64_t grid = cdiv(line, per_cta);
+  return int32_t(grid < most ? grid : most);
+}
+
+Plan make_plan(const sparge_kv4_t& c, const sparge_kv4_attn_t& a) {
+  Plan p{};
+  int64_t rows = int64_t(a.max_q) * (a.Hq / c.Hkv);
+  if (rows > kFewRows) {
+    // a unit's start costs twelve steps, so shorter lines take no more CTAs
+    p.piece_grid = grid_of(c, a, cdiv(rows, kPieceRows), 64, kSms, 1);
+    if (a.R == 1) return p;
+    rows = kFewRows;  // the other requests may bring few
+  }
+  p.nt = rows <= 8 ? 1 : 2;
+  p.grid = grid_of(c, a, cdiv(rows, 8 * p.nt), 32, kSms * ctas_per_sm(p.nt), kWarps);
   return p;
 }
 
 // Of one size for every call, so that calls of different shapes may share a
 // workspace: no other region ever lies on the counters.
-size_t arrived_bytes(const Plan&) {
-  return align256(size_t(kSms) * ctas_per_sm(1) * sizeof(uint32_t));
+size_t arrived_bytes() { return align256(size_t(kSms) * ctas_per_sm(1) * sizeof(uint32_t)); }
+size_t part_rows(const Plan& p) {
+  const size_t few = size_t(p.grid) * 2 * 8 * p.nt, piece = size_t(p.piece_grid) * 2 * kPieceRows;
+  return few > piece ? few : piece;
 }
-size_t ml_bytes(const Plan& p) { return align256(size_t(p.grid) * 2 * 8 * p.nt * sizeof(float2)); }
+size_t ml_bytes(const Plan& p) { return align256(part_rows(p) * sizeof(float2)); }
 
 template <int D, int NG, int NT>
 cudaError_t run(const DecodeArgs& a, const Plan& p, cudaStream_t stream) {
@@ -902,7 +788,7 @@ cudaError_t run_nt(const DecodeArgs& a, const Plan& p, cudaStream_t s) {
 
 size_t kv4_attn_ws_bytes(const sparge_kv4_t& c, const sparge_kv4_attn_t& a) {
   const Plan p = make_plan(c, a);
-  return 256 + arrived_bytes(p) + ml_bytes(p) + size_t(p.grid) * 2 * 8 * p.nt * c.d * sizeof(float);
+  return 256 + arrived_bytes() + ml_bytes(p) + part_rows(p) * c.d * sizeof(float);
 }
 
 cudaError_t launch_kv4_attn(const sparge_kv4_t& c, const sparge_kv4_attn_t& a, const void* q,
@@ -920,8 +806,8 @@ cudaError_t launch_kv4_attn(const sparge_kv4_t& c, const sparge_kv4_attn_t& a, c
   d.lse = lse;
   d.status = static_cast<int32_t*>(ws);
   d.arrived = ws_ptr<uint32_t>(ws, 256);
-  d.part_ml = ws_ptr<float2>(ws, 256 + arrived_bytes(p));
-  d.part_o = ws_ptr<float>(ws, 256 + arrived_bytes(p) + ml_bytes(p));
+  d.part_ml = ws_ptr<float2>(ws, 256 + arrived_bytes());
+  d.part_o = ws_ptr<float>(ws, 256 + arrived_bytes() + ml_bytes(p));
   d.q_stride = a.q_stride * 2;
   d.R = a.R;
   d.T = a.T;
@@ -936,11 +822,19 @@ cudaError_t launch_kv4_attn(const sparge_kv4_t& c, const sparge_kv4_attn_t& a, c
   d.causal = a.causal;
   d.num_pages = c.num_pages;
   d.bf16 = a.dtype == SPARGE_BF16;
-  d.masks = Masks{0x000F000Fu, 0x00F000F0u};
+  d.masks = Masks{0x000F000Fu, 0x00F000F0u, 0x00F0000Fu};
   d.scale_log2 = a.scale * 1.4426950408889634f;
   const int ng = c.d / c.group;
-  if (c.d == 64)
-    return ng == 2 ? run_nt<64, 2>(d, p, stream) : run_nt<64, 1>(d, p, stream);
+  d.min_rows = 0;
+  d.max_rows = INT32_MAX;
+  if (p.piece_grid > 0) {
+    if (p.grid > 0) d.min_rows = kFewRows + 1;
+    const cudaError_t e = launch_kv4_piece(d, c.d, ng, p.piece_grid, stream);
+    if (e != cudaSuccess || p.grid == 0) return e;
+    d.min_rows = 0;
+    d.max_rows = kFewRows;
+  }
+  if (c.d == 64) return ng == 2 ? run_nt<64, 2>(d, p, stream) : run_nt<64, 1>(d, p, stream);
   if (ng == 4) return run_nt<128, 4>(d, p, stream);
   return ng == 2 ? run_nt<128, 2>(d, p, stream) : run_nt<128, 1>(d, p, stream);
 }

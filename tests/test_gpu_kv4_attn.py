@@ -227,3 +227,49 @@ def test_binding_refusals():
     for kw in bad:
         with pytest.raises(fb.SpargeError):
             fb.sparge_kv4_attn(**{**good, **kw})
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d,group", SHAPES)
+@pytest.mark.parametrize("lens,news,Hq,Hkv", [
+    ([33], [33], 1, 1), ([129, 64, 300], [129, 17, 257], 4, 2), ([2000, 63, 700, 5], [40, 1, 300, 5], 8, 1),
+    ([9000], [70], 6, 2), ([1500, 1400], [513, 64], 5, 5)])
+def test_pieces_of_prompts(lens, news, Hq, Hkv, d, group, dtype):
+    """Many rows per request: one and two tiles of 128 rows, part tiles, units cut over CTAs, and
+    requests with few rows in the same call."""
+    for causal in (True, False):
+        check(AttnCase(fb, dev(), lens, news, Hq, Hkv, d, group, 48, dtype, seed=sum(lens), pad=2), causal=causal)
+
+
+def test_pieces_leave_unseen_keys_out():
+    """As for few rows: NaN behind the last token, keys of the future that are NaN, a bad page."""
+    case = AttnCase(fb, dev(), [200, 300], [70, 64], 4, 2, 64, 32, 16, torch.float16, stale=False)
+    check(case)
+    want = case.exact()
+    bad = torch.full((1, 2, 64), float("nan"), dtype=torch.float16, device=dev())
+    one = torch.ones_like(bad)
+    fb.sparge_kv4_append(case.c, bad, one, case.slots[0][-1:], case.cache)      # K alone
+    fb.sparge_kv4_append(case.c, one, bad, case.slots[1][-2:-1], case.cache)    # V alone
+    o, lse = case.run()
+    nan_rows = [69, 70 + 62, 70 + 63]
+    rest = [i for i in range(134) if i not in nan_rows]
+    assert bool(o[nan_rows].isnan().all())
+    keep = lambda x: x[rest]
+    case.T, case.pad = len(rest), 0
+    check_attn(case, (keep(o), keep(lse)), tuple(keep(x) for x in want))
+
+
+def test_pieces_with_extreme_values():
+    for dtype, kscale, vscale in ((torch.bfloat16, 1.0, 1e5), (torch.bfloat16, 1e5, 1.0),
+                                  (torch.float16, 1.0, 2e4), (torch.float16, 1.0, 0.02)):
+        check(AttnCase(fb, dev(), [150], [100], 4, 2, 128, 64, 16, dtype, q_scale=2.0 / max(kscale, 1.0),
+                       kscale=kscale, vscale=vscale))
+
+
+def test_pieces_same_bits_and_counters():
+    case = AttnCase(fb, dev(), [5000, 900], [90, 200], 8, 2, 128, 32, 64, torch.bfloat16)
+    o, lse = check(case)
+    for _ in range(3):
+        a, b = case.run(ws=case.ws)
+        torch.cuda.synchronize()
+        assert torch.equal(a, o) and torch.equal(b, lse)
