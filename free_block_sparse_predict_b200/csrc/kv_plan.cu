@@ -26,7 +26,6 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanPer = 4;  // requests per thread
-constexpr int kRun = 8;      // tokens per thread and step
 constexpr int kBatch = 8;    // pages that come back, in flight per thread
 constexpr int kPlanMax = kPlanThreads * kPlanPer;
 static_assert(kPlanMax == kMaxPlanRequests, "every request has a thread");
@@ -69,6 +68,8 @@ __device__ __forceinline__ int32_t pages_of(int32_t tokens, int32_t P) {
   return int32_t((uint32_t(tokens) + uint32_t(P) - 1u) / uint32_t(P));
 }
 
+// RUN: consecutive tokens per thread and step.
+template <int RUN>
 __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs A) {
   namespace cg = cooperative_groups;
   const cg::cluster_group cluster = cg::this_cluster();
@@ -184,18 +185,18 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
   }
   cluster.sync();  // the pushed pages are there
 
-  // ---- slots: kRun consecutive tokens per thread and step, so that the search
+  // ---- slots: RUN consecutive tokens per thread and step, so that the search
   // for the request is paid once for them; the first token of a new page writes
   // its table entry
   const int32_t end = s_cu[A.R];
-  const int64_t runs = (int64_t(A.max_tokens) + kRun - 1) / kRun;
+  const int64_t runs = (int64_t(A.max_tokens) + RUN - 1) / RUN;
   const bool vec = (reinterpret_cast<uintptr_t>(A.slot_map) & 15u) == 0;
   for (int64_t n = int64_t(rank) * kPlanThreads + threadIdx.x; n < runs;
        n += int64_t(ctas) * kPlanThreads) {
-    const int32_t t0 = int32_t(n * kRun);
-    int32_t slot[kRun];
+    const int32_t t0 = int32_t(n * RUN);
+    int32_t slot[RUN];
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) slot[i] = -1;
+    for (int i = 0; i < RUN; ++i) slot[i] = -1;
     if (t0 < end) {
       int r = 0, hi = A.R;  // the last request that starts at or before t0
       while (hi - r > 1) {
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
         return id;
       };
       const auto first_slot = [&](int32_t id) { return int32_t(uint32_t(id) * uint32_t(P)); };
-      if (t0 + kRun <= s_cu[r + 1] && P >= kRun) {
+      if (RUN > 1 && t0 + RUN <= s_cu[r + 1] && P >= RUN) {
         // all of one request and of one or two of its pages: nearly every run
         const int32_t len = s_len[r];
         if (len >= 0) {
@@ -220,14 +221,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
           const int32_t in = pos - p * P;
           const int32_t a = first_slot(page_id(r, p, have, in == 0)) + in;
           int32_t b = 0;  // so that b + i is token i's slot, if it is in the next page
-          if (in + kRun > P) b = first_slot(page_id(r, p + 1, have, true)) + in - P;
+          if (in + RUN > P) b = first_slot(page_id(r, p + 1, have, true)) + in - P;
 #pragma unroll
-          for (int i = 0; i < kRun; ++i) slot[i] = (in + i < P ? a : b) + i;
+          for (int i = 0; i < RUN; ++i) slot[i] = (in + i < P ? a : b) + i;
         }
       } else {
         int32_t next = s_cu[r + 1];    // where the request's tokens end
         int32_t in = P, slot_at = -1;  // offset in the page at hand (P: none), next slot
-        for (int i = 0; i < kRun && t0 + i < end; ++i) {
+        for (int i = 0; i < RUN && t0 + i < end; ++i) {
           const int32_t t = t0 + i;
           while (t >= next) next = s_cu[++r + 1], in = P;
           const int32_t len = s_len[r];
@@ -238,37 +239,36 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
             slot_at = first_slot(page_id(r, p, pages_of(len, P), in == 0)) + in;
           }
 #pragma unroll
-          for (int k = 0; k < kRun; ++k)
+          for (int k = 0; k < RUN; ++k)
             if (k == i) slot[k] = slot_at;
           ++slot_at;
           ++in;
         }
       }
     }
-    if (vec && t0 + kRun <= A.max_tokens) {
+    if (RUN % 4 == 0 && vec && t0 + RUN <= A.max_tokens) {
 #pragma unroll
-      for (int i = 0; i < kRun; i += 4)
+      for (int i = 0; i + 3 < RUN; i += 4)
         *reinterpret_cast<int4*>(A.slot_map + t0 + i) =
             make_int4(slot[i], slot[i + 1], slot[i + 2], slot[i + 3]);
     } else {
 #pragma unroll
-      for (int i = 0; i < kRun; ++i)
+      for (int i = 0; i < RUN; ++i)
         if (t0 + i < A.max_tokens) A.slot_map[t0 + i] = slot[i];
     }
   }
 }
 
-}  // namespace
-
-cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
+template <int RUN>
+cudaError_t run(const KvPlanArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  // a thread for kRun tokens, up to sixteen CTAs
-  const int64_t ctas = cdiv(a.max_tokens, int64_t(kRun) * kPlanThreads);
+  // a thread for RUN tokens, up to sixteen CTAs
+  const int64_t ctas = cdiv(a.max_tokens, int64_t(RUN) * kPlanThreads);
   int n = 1;
   while (n < 16 && n < ctas) n <<= 1;
   if (n > 8) {  // more than the portable cluster size
-    const cudaError_t e =
-        cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t e = cudaFuncSetAttribute(
+        plan_kernel<RUN>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
   cfg.gridDim = dim3(unsigned(n));
@@ -276,7 +276,7 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
   cfg.dynamicSmemBytes = (3 * size_t(a.R) + 1) * sizeof(int32_t);
   if (cfg.dynamicSmemBytes > 46 * 1024) {  // 48 KB with the static part need no permission
     const cudaError_t e =
-        cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaFuncSetAttribute(plan_kernel<RUN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int((3 * kPlanMax + 1) * sizeof(int32_t)));
     if (e != cudaSuccess) return e;
   }
@@ -287,7 +287,16 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, plan_kernel, a);
+  return cudaLaunchKernelEx(&cfg, plan_kernel<RUN>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
+  // A decode step has about a token per request: a thread each (run together
+  // they would fetch their eight requests' pages one after the other, 9.9
+  // instead of PLANSTEP us for 256).  Prompts' tokens share requests and pages.
+  return a.max_tokens <= 4 * kPlanThreads ? run<1>(a, stream) : run<8>(a, stream);
 }
 
 }  // namespace sparge

@@ -23,6 +23,9 @@ namespace sparge {
 namespace {
 
 constexpr int kRopeThreads = 256;
+// Three CTAs a SM (85 registers): two left the loads too few (414 us for the
+// 1.07 GB of a 128K prompt's queries against 349), four spilled (384 us).
+constexpr int kRopeCtas = 3;
 constexpr int kBatch = 4;  // heads whose vectors are in flight at once
 
 template <int DT>
@@ -120,7 +123,7 @@ __device__ __forceinline__ void turn_pairs(uint4& ra, uint4& rb, const float* cs
 }
 
 template <int DT, bool IL>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs P) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const RopeArgs P) {
   using T = RopeType<DT>;
   constexpr int V = T::V;
   const int64_t item = int64_t(blockIdx.x) * kRopeThreads + threadIdx.x;
@@ -144,6 +147,23 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs P) {
 
   for (int32_t bg = blockIdx.y; bg < P.B * P.groups; bg += gridDim.y) {
     const int32_t b = bg / P.groups, g = bg - b * P.groups;
+    const int32_t h1 = min(P.H, (g + 1) * P.heads);
+    const char* src = P.src + b * P.ss[0] + int64_t(P.inverse ? p : s) * P.ss[2];
+    char* dst = P.dst + b * P.ds[0] + int64_t(P.inverse ? s : p) * P.ds[2];
+    // kBatch heads' loads before their stores: x and y may be one tensor (each
+    // vector is touched by one thread only), so the compiler keeps the order
+    uint4 ra[kBatch], rb[kBatch];
+    auto load = [&](int32_t h0) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (h0 + i < h1) {
+          const uint4* x = reinterpret_cast<const uint4*>(src + (h0 + i) * P.ss[1]);
+          ra[i] = x[va];
+          if (two) rb[i] = x[vb];
+        }
+      }
+    };
+    load(g * P.heads);  // in flight while the angles are computed
     float cs[V], sn[V];
     if (turn) {
       const int32_t* pos = P.pos + b * P.pos_stride;
@@ -160,21 +180,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs P) {
         if (P.inverse) sn[k] = -sn[k];
       }
     }
-    const int32_t h1 = min(P.H, (g + 1) * P.heads);
-    const char* src = P.src + b * P.ss[0] + int64_t(P.inverse ? p : s) * P.ss[2];
-    char* dst = P.dst + b * P.ds[0] + int64_t(P.inverse ? s : p) * P.ds[2];
-    // kBatch heads' loads before their stores: x and y may be one tensor (each
-    // vector is touched by one thread only), so the compiler keeps the order
     for (int32_t h0 = g * P.heads; h0 < h1; h0 += kBatch) {
-      uint4 ra[kBatch], rb[kBatch];
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (h0 + i < h1) {
-          const uint4* x = reinterpret_cast<const uint4*>(src + (h0 + i) * P.ss[1]);
-          ra[i] = x[va];
-          if (two) rb[i] = x[vb];
-        }
-      }
+      if (h0 > g * P.heads) load(h0);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         if (h0 + i >= h1) break;
