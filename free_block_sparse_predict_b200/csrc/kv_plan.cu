@@ -10,15 +10,16 @@
 // All sums are prefix sums over the requests, so the result does not depend on
 // timing.  Latency-bound: a few KB of metadata, then 4 bytes written per token.
 //
-// One cluster of CTAs does it in one launch.  Every CTA takes the prefix sums
-// over all requests for itself (they are in L2 after the first), all inputs
-// that may be outputs too are read before the first cluster barrier and
-// written behind it, and the pages pushed by the first CTA are read by the
-// others behind the second.
+// One launch does it, with one barrier over its CTAs.  Every CTA takes the prefix
+// sums over all requests for itself (they are in L2 after the first).  Before
+// the barrier all inputs that may be outputs too are read, and the pages of
+// ended requests are pushed (above the stack's top, where nothing else is read);
+// behind it the outputs are written and the new pages are taken.
 #include <cooperative_groups.h>
 
 #include <cstdint>
 
+#include "div.cuh"
 #include "sparge_internal.h"
 
 namespace sparge {
@@ -64,16 +65,17 @@ __device__ __forceinline__ void block_scan(int64_t (&v)[N], int64_t* sh, int64_t
   }
 }
 
-__device__ __forceinline__ int32_t pages_of(int32_t tokens, int32_t P) {
-  return int32_t((uint32_t(tokens) + uint32_t(P) - 1u) / uint32_t(P));
+// Pages of that many tokens, 0 <= tokens < 2^31.
+__device__ __forceinline__ int32_t pages_of(int32_t tokens, const Div& page) {
+  return tokens > 0 ? page.quot(tokens - 1) + 1 : 0;
 }
 
-// RUN: consecutive tokens per thread and step.
-template <int RUN>
-__global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs A) {
+// RUN: consecutive tokens per thread and step.  GRID: the CTAs are the whole
+// cooperative grid instead of one cluster.
+template <int RUN, bool GRID>
+__global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs A, const Div page) {
   namespace cg = cooperative_groups;
-  const cg::cluster_group cluster = cg::this_cluster();
-  const int rank = int(cluster.block_rank()), ctas = int(cluster.num_blocks());
+  const int rank = int(blockIdx.x), ctas = int(gridDim.x);
   __shared__ int64_t sh1[64], sh2[32];
   __shared__ unsigned long long s_popped;
   extern __shared__ int32_t s_dyn[];
@@ -102,7 +104,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
       n[i] = A.new_len[r];
     }
     if (n[i] > 0) sums[0] += n[i];
-    if (n[i] < 0) sums[1] += pages_of(L[i], P);
+    if (n[i] < 0) sums[1] += pages_of(L[i], page);
   }
   int64_t totals[2];
   block_scan(sums, sh1, totals);
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
     if (n[i] > 0) {
       at += n[i];
       if (after <= cap && at <= A.max_tokens)
-        want[i] = pages_of(int32_t(after), P) - pages_of(L[i], P);
+        want[i] = pages_of(int32_t(after), page) - pages_of(L[i], page);
     }
     if (want[i] > 0) upto[0] += want[i];
   }
@@ -142,14 +144,35 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
     if (n[i] > 0) cu += n[i];
     if (n[i] < 0) {
       s_len[r] = -2 - L[i];  // ended
-      put += pages_of(L[i], P);
+      put += pages_of(L[i], page);
     }
   }
   if (threadIdx.x == 0) s_cu[A.R] = int32_t(tokens > INT32_MAX ? INT32_MAX : tokens);
   // needs grow along the requests, so what is taken is the largest sum admitted
   if (popped > 0) atomicMax(&s_popped, (unsigned long long)popped);
 
-  cluster.sync();  // every CTA has read what the first one now overwrites
+  // ---- pages of ended requests, a warp per request
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  for (int r = int(threadIdx.x >> 5) * ctas + rank; r < A.R; r += kPlanThreads / 32 * ctas) {
+    if (s_len[r] > -2) continue;
+    const int pages = pages_of(-2 - s_len[r], page);
+    const int32_t* row = A.block_table + int64_t(r) * A.max_pages;
+    int32_t* to = A.free_pages + count + s_off[r];
+    const int room = int(min(int64_t(pages), A.num_pages - count - s_off[r]));
+    for (int j0 = lane; j0 < room; j0 += 32 * kBatch) {
+      int32_t id[kBatch];  // loads first: one latency for all
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (j0 + 32 * k < room) id[k] = row[j0 + 32 * k];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (j0 + 32 * k < room) to[j0 + 32 * k] = id[k];
+    }
+  }
+
+  if (GRID) cg::this_grid().sync(); else cg::this_cluster().sync();
+
   if (rank == 0) {
 #pragma unroll
     for (int i = 0; i < kPlanPer; ++i) {
@@ -164,26 +187,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
       A.cu_new[A.R] = s_cu[A.R];
       *A.free_count_out = int32_t(avail - int64_t(s_popped));
     }
-    // pages of ended requests, a warp per request
-    const int lane = threadIdx.x & 31;
-    for (int r = threadIdx.x >> 5; r < A.R; r += kPlanThreads / 32) {
-      if (s_len[r] > -2) continue;
-      const int pages = pages_of(-2 - s_len[r], P);
-      const int32_t* row = A.block_table + int64_t(r) * A.max_pages;
-      int32_t* to = A.free_pages + count + s_off[r];
-      const int room = int(min(int64_t(pages), A.num_pages - count - s_off[r]));
-      for (int j0 = lane; j0 < room; j0 += 32 * kBatch) {
-        int32_t id[kBatch];  // loads first: one latency for all
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          if (j0 + 32 * k < room) id[k] = row[j0 + 32 * k];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          if (j0 + 32 * k < room) to[j0 + 32 * k] = id[k];
-      }
-    }
   }
-  cluster.sync();  // the pushed pages are there
 
   // ---- slots: RUN consecutive tokens per thread and step, so that the search
   // for the request is paid once for them; the first token of a new page writes
@@ -217,7 +221,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
         // all of one request and of one or two of its pages: nearly every run
         const int32_t len = s_len[r];
         if (len >= 0) {
-          const int32_t pos = len + (t0 - s_cu[r]), p = pos / P, have = pages_of(len, P);
+          const int32_t pos = len + (t0 - s_cu[r]), p = page.quot(pos), have = pages_of(len, page);
           const int32_t in = pos - p * P;
           const int32_t a = first_slot(page_id(r, p, have, in == 0)) + in;
           int32_t b = 0;  // so that b + i is token i's slot, if it is in the next page
@@ -234,9 +238,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
           const int32_t len = s_len[r];
           if (len < 0) continue;
           if (in == P) {  // another page
-            const int32_t pos = len + (t - s_cu[r]), p = pos / P;
+            const int32_t pos = len + (t - s_cu[r]), p = page.quot(pos);
             in = pos - p * P;
-            slot_at = first_slot(page_id(r, p, pages_of(len, P), in == 0)) + in;
+            slot_at = first_slot(page_id(r, p, pages_of(len, page), in == 0)) + in;
           }
 #pragma unroll
           for (int k = 0; k < RUN; ++k)
@@ -259,44 +263,51 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
   }
 }
 
-template <int RUN>
-cudaError_t run(const KvPlanArgs& a, cudaStream_t stream) {
+template <int RUN, bool GRID>
+cudaError_t run(const KvPlanArgs& a, int max_ctas, cudaStream_t stream) {
+  const auto kernel = plan_kernel<RUN, GRID>;
   cudaLaunchConfig_t cfg{};
-  // a thread for RUN tokens, up to sixteen CTAs
+  // a thread for RUN tokens, up to max_ctas CTAs
   const int64_t ctas = cdiv(a.max_tokens, int64_t(RUN) * kPlanThreads);
   int n = 1;
-  while (n < 16 && n < ctas) n <<= 1;
-  if (n > 8) {  // more than the portable cluster size
-    const cudaError_t e = cudaFuncSetAttribute(
-        plan_kernel<RUN>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
+  if (GRID) n = int(ctas < max_ctas ? ctas : max_ctas);
+  while (!GRID && n < max_ctas && n < ctas) n <<= 1;
   cfg.gridDim = dim3(unsigned(n));
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = (3 * size_t(a.R) + 1) * sizeof(int32_t);
   if (cfg.dynamicSmemBytes > 46 * 1024) {  // 48 KB with the static part need no permission
-    const cudaError_t e =
-        cudaFuncSetAttribute(plan_kernel<RUN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int((3 * kPlanMax + 1) * sizeof(int32_t)));
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               int((3 * kPlanMax + 1) * sizeof(int32_t)));
     if (e != cudaSuccess) return e;
   }
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(n);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  if (GRID) {
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(n);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  }
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, plan_kernel<RUN>, a);
+  return cudaLaunchKernelEx(&cfg, kernel, a, make_div(uint32_t(a.page_size)));
 }
 
 }  // namespace
 
 cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
-  // A decode step has about a token per request: a thread each (run together
-  // they would fetch their eight requests' pages one after the other, 9.9
-  // instead of PLANSTEP us for 256).  Prompts' tokens share requests and pages.
-  return a.max_tokens <= 4 * kPlanThreads ? run<1>(a, stream) : run<8>(a, stream);
+  // A decode step has about a token per request: a thread each (runs of eight
+  // would fetch eight requests' pages one after the other, 9.9 instead of 5.9 us
+  // for 256), in a cluster of eight at most.  Prompts' tokens share requests and
+  // pages, and writing their slots wants every SM: 10.7 us for 500 prompts of up
+  // to 4096 tokens, 29 us in a cluster of sixteen.  The grid's barrier costs
+  // about 2 us more than a cluster's: 16,000 tokens take 7.3 us in a cluster and
+  // 9.3 us in the grid, 64,000 tokens 13.6 and 8.7 us.
+  constexpr int kSms = 148, kCluster = 8;
+  return a.max_tokens <= 4 * kCluster * kPlanThreads ? run<1, false>(a, kCluster, stream)
+                                                     : run<4, true>(a, kSms, stream);
 }
 
 }  // namespace sparge

@@ -22,7 +22,8 @@ def run(args, tokens, in_place=False):
 
 @pytest.mark.parametrize("R,P,width,new_max", [
     (1, 16, 3, 5), (7, 16, 40, 200), (33, 64, 9, 1), (200, 1, 50, 30), (500, 48, 20, 700),
-    (1024, 16, 8, 20), (1025, 32, 5, 1), (4096, 16, 4, 9), (3, 128, 400, 40000)])
+    (1024, 16, 8, 20), (1025, 32, 5, 1), (4096, 16, 4, 9), (3, 128, 400, 40000),
+    (4000, 16, 9, 100), (300, 7, 90, 600)])
 @pytest.mark.parametrize("spare", [1.0, 0.6, 0.0])
 def test_matches_the_definition(R, P, width, new_max, spare):
     rng = np.random.default_rng(R + int(10 * spare))
@@ -32,6 +33,12 @@ def test_matches_the_definition(R, P, width, new_max, spare):
     run(args, total, in_place=True)
     run(args, max(0, total // 2))                 # slots for half of the tokens only
     run(args, 0)
+
+
+def test_many_padding_slots():
+    """More slots than a whole grid of threads writes at once, nearly all of them padding."""
+    rng = np.random.default_rng(9)
+    run(random_plan(rng, 5, 16, 30, 300), 700_001, in_place=True)
 
 
 def test_ends_only_and_idle_only():
