@@ -49,7 +49,6 @@ static_assert(kFeedRegs + kCodeRegs + 2 * kRowRegs <= 4 * kLaunchRegs, "register
 constexpr int kTile = 128;           // rows of an MMA
 constexpr int kRows = 2 * kTile;     // rows of a unit
 constexpr int kKeys = 64;            // keys of a step
-constexpr int kRaw = 4;              // steps of codes in flight
 constexpr int kFlags = 16;           // steps whose tiles' validity is remembered
 constexpr float kRescale = 8.0f;     // log2 units
 // A unit's start and end in steps: its queries, the pipeline's filling, the
@@ -64,18 +63,21 @@ struct PieceCfg {
   static constexpr int PARTS = SPLIT ? 2 : 1;          // tiles that add up to K, and to V
   static constexpr int ONE = kKeys * D * 2;
   static constexpr int KV = PARTS * ONE;               // K or V of a step
-  static constexpr int K = 0, V = 2 * KV, CODE = 4 * KV;
-  static constexpr int SMEM = CODE + kRaw * RAW;
-  // tensor memory per tile: S, overwritten by P | Q in fp16 | O
-  static constexpr int TILE_COLS = 256, Q_COL = 64, O_COL = 128;
+  static constexpr int QT = kTile * D * 2;             // a tile's queries
+  static constexpr int Q = 0, K = 2 * QT, V = K + 2 * KV, CODE = V + 2 * KV;
+  static constexpr int STAGES = SPLIT && D == 128 ? 3 : 4;  // steps of codes in flight: what fits
+  static constexpr int SMEM = CODE + STAGES * RAW;
+  // tensor memory per tile: S of even steps, of odd steps, each overwritten by its P | O
+  static constexpr int TILE_COLS = 256, O_COL = 128;
   static_assert(SMEM + 4096 <= 227 * 1024, "one CTA per SM");
 };
 
 struct PieceBars {
-  uint64_t raw_full[kRaw], raw_empty[kRaw];
+  uint64_t raw_full[4], raw_empty[4];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2];  // per tile
-  uint64_t o_final[2];            // a part's last O += P V
+  // per tile and parity of the step, since either side may be a step ahead of the
+  // other's last look
+  uint64_t s_full[2][2], p_full[2][2], o_done[2][2];
   uint64_t drain;
 };
 
@@ -184,12 +186,13 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
 
   if (threadIdx.x == 0) {
     s_abort = 0;
-    for (int i = 0; i < kRaw; ++i) mbar_init(&bars.raw_full[i], 1), mbar_init(&bars.raw_empty[i], 4);
+    for (int i = 0; i < C::STAGES; ++i) mbar_init(&bars.raw_full[i], 1), mbar_init(&bars.raw_empty[i], 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.k_full[i], 4), mbar_init(&bars.k_empty[i], 1);
       mbar_init(&bars.v_full[i], 4), mbar_init(&bars.v_empty[i], 1);
-      mbar_init(&bars.s_full[i], 1), mbar_init(&bars.p_full[i], 4);
-      mbar_init(&bars.o_final[i], 1);
+      for (int k = 0; k < 2; ++k)
+        mbar_init(&bars.s_full[i][k], 1), mbar_init(&bars.p_full[i][k], 4),
+            mbar_init(&bars.o_done[i][k], 1);
     }
     mbar_init(&bars.drain, 1);
     fence_mbar_init();
@@ -277,10 +280,10 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
                 atomicCAS(A.status, 0, int32_t(SPARGE_EINVAL));
             }
           }
-          const uint32_t n = g + t, stage = n % kRaw;
-          if (n >= kRaw)
+          const uint32_t n = g + t, stage = n % C::STAGES;
+          if (n >= C::STAGES)
             ok = __all_sync(0xffffffffu,
-                            mbar_wait(&bars.raw_empty[stage], (n / kRaw - 1) & 1, abort, A.status));
+                            mbar_wait(&bars.raw_empty[stage], (n / C::STAGES - 1) & 1, abort, A.status));
           if (!ok) break;
           const uint32_t there =
               __ballot_sync(0xffffffffu, id >= 0) >> (4 * (t & 7)) & 15u;
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
       }
       // copies in flight land before the CTA can end
       if (!ok && lane == 0)
-        for (int s = 0; s < kRaw; ++s) {
+        for (int s = 0; s < C::STAGES; ++s) {
           mbar_wait_teardown(&bars.raw_full[s], 0);
           mbar_wait_teardown(&bars.raw_full[s], 1);
         }
@@ -316,67 +319,64 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
       const uint32_t idesc_qk = instr_desc(1, 0, 0, 0, kTile, kKeys);
       const uint32_t idesc_pv = instr_desc(1, 0, 0, 1, kTile, D);
       // Descriptors step by their addresses' field, 16 bytes a unit
+      const uint64_t dq = smem_desc(smem_u32(smem + C::Q), 16, 1024);
       const uint64_t dk = smem_desc(smem_u32(smem + C::K), 16, 1024);
       const uint64_t dv = smem_desc(smem_u32(smem + C::V), kKeys * 128, 1024);
       while (next_part(A, line, p)) {
         __syncthreads();
         tc_fence_after();
         const int tiles = p.two ? 2 : 1;
-        if (lane == 0) {
+        if (elect_one()) {
           auto scores = [&](int i, int t) {  // S of tile i and step t
-            const uint32_t base = tmem + uint32_t(i * C::TILE_COLS), b = (g + t) & 1;
+            const uint32_t m = gt[i] + t, b = (g + t) & 1;
+            const uint32_t at = tmem + uint32_t(i * C::TILE_COLS) + (m & 1) * kKeys;
 #pragma unroll
             for (int kk = 0; kk < C::PARTS * (D / 16); ++kk) {
               const int slab = kk % (D / 16) / 4, within = (kk % 4) * 32, rest = kk / (D / 16);
-              mma_f16_ts(base, base + C::Q_COL + kk % (D / 16) * 8,
+              mma_f16_ss(at, dq + (i * C::QT + slab * (kTile * 128) + within) / 16,
                          dk + b * (C::KV / 16) +
                              (rest * C::ONE + slab * (kKeys * 128) + within) / 16,
                          idesc_qk, kk > 0 ? 1u : 0u);
             }
-            mma_commit(&bars.s_full[i]);
+            mma_commit(&bars.s_full[i][m & 1]);
           };
           auto values = [&](int i, int t) {  // O += P V
-            const uint32_t base = tmem + uint32_t(i * C::TILE_COLS), b = (g + t) & 1;
+            const uint32_t m = gt[i] + t, b = (g + t) & 1;
+            const uint32_t base = tmem + uint32_t(i * C::TILE_COLS);
 #pragma unroll
             for (int kk = 0; kk < C::PARTS * (kKeys / 16); ++kk) {
               const int step = kk % (kKeys / 16), rest = kk / (kKeys / 16);
-              mma_f16_ts(base + C::O_COL, base + step * 8,
+              mma_f16_ts(base + C::O_COL, base + (m & 1) * kKeys + step * 8,
                          dv + b * (C::KV / 16) + (rest * C::ONE + step * 2048) / 16, idesc_pv,
                          (t > 0 || kk > 0) ? 1u : 0u);
             }
+            mma_commit(&bars.o_done[i][m & 1]);
           };
-          auto keys_there = [&](int t) {
+          auto all_scores = [&](int t) {
             const uint32_t n = g + t;
             if (!mbar_wait(&bars.k_full[n & 1], (n >> 1) & 1, abort, A.status)) return false;
             tc_fence_after();
+            for (int i = 0; i < tiles; ++i) scores(i, t);
+            mma_commit(&bars.k_empty[n & 1]);
             return true;
           };
-          // Each tile's order is S, P V, the next S, ...: S's columns are free once
-          // P V, which reads P there, has been issued before it, and a tile's scores
-          // are announced with all products before them done, O among them.
-          if (ok && p.n > 0 && (ok = keys_there(0))) {
-            for (int i = 0; i < tiles; ++i) scores(i, 0);
-            mma_commit(&bars.k_empty[g & 1]);
-          }
+          // S of the next step comes before P V of this one, so that the softmax need
+          // not wait for it; its columns were those of P two steps back, whose P V has
+          // been issued before it.
+          if (ok && p.n > 0) ok = all_scores(0);
           for (int t = 0; t < p.n && ok; ++t) {
             const uint32_t n = g + t, b = n & 1;
+            if (t + 1 < p.n && !(ok = all_scores(t + 1))) break;
             for (int i = 0; i < tiles && ok; ++i) {
               const uint32_t m = gt[i] + t;
-              ok = mbar_wait(&bars.p_full[i], m & 1, abort, A.status) &&
+              ok = mbar_wait(&bars.p_full[i][m & 1], (m >> 1) & 1, abort, A.status) &&
                    (i > 0 || mbar_wait(&bars.v_full[b], (n >> 1) & 1, abort, A.status));
               if (!ok) break;
               tc_fence_after();
               values(i, t);
-              if (t + 1 == p.n) {
-                mma_commit(&bars.o_final[i]);
-              } else {
-                if (i == 0 && !(ok = keys_there(t + 1))) break;
-                scores(i, t + 1);
-              }
             }
             if (!ok) break;
             mma_commit(&bars.v_empty[b]);
-            if (t + 1 < p.n) mma_commit(&bars.k_empty[b ^ 1]);
           }
           if (!ok && !drained) {
             give_up();
@@ -406,9 +406,9 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
     while (next_part(A, line, p)) {
       __syncthreads();
       for (int t = 0; t < p.n && ok; ++t) {
-        const uint32_t n = g + t, stage = n % kRaw, b = n & 1;
+        const uint32_t n = g + t, stage = n % C::STAGES, b = n & 1;
         ok = __all_sync(0xffffffffu,
-                        mbar_wait(&bars.raw_full[stage], (n / kRaw) & 1, abort, A.status) &&
+                        mbar_wait(&bars.raw_full[stage], (n / C::STAGES) & 1, abort, A.status) &&
                             (n < 2 || mbar_wait(&bars.k_empty[b], ((n >> 1) - 1) & 1, abort, A.status)));
         if (!ok) break;
         const uint8_t* raw = smem + C::CODE + stage * C::RAW;
@@ -509,7 +509,6 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
     // =================================================== softmax
     regs_up<kRowRegs>();
     const int tile = (warp - 8) >> 2, quad = warp & 3, r = quad * 32 + lane;
-    uint32_t ended = 0;  // parts in which the tile had steps
     const uint32_t at = tmem + uint32_t(tile * C::TILE_COLS) + (uint32_t(quad * 32) << 16);
     while (next_part(A, line, p)) {
       const int row = p.row0 + tile * kTile + r;
@@ -559,8 +558,12 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
       }
       if (active) {
 #pragma unroll
-        for (int w = 0; w < D / 64; ++w) tmem_st32(at + C::Q_COL + 32 * w, qw[w]);
-        tmem_wait_st();
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t* w = &qw[i / 8][4 * (i % 8)];
+          *reinterpret_cast<uint4*>(smem + C::Q + tile * C::QT + i / 8 * (kTile * 128) +
+                                    swizzled(r, i % 8)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_async_shared();
       }
       tc_fence_before();
       __syncthreads();  // the queries are there
@@ -568,16 +571,17 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
       float m = -INFINITY, l = 0.f;  // the maximum P is scaled by, and the sum
       const int steps = active ? p.n : 0;
       for (int t = 0; t < steps; ++t) {
-        const uint32_t n = gt[tile] + t;
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars.s_full[tile], n & 1, abort, A.status));
+        const uint32_t n = gt[tile] + t, at_s = at + (n & 1) * kKeys;
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(&bars.s_full[tile][n & 1], (n >> 1) & 1, abort, A.status));
         if (!ok) break;
         tc_fence_after();
         uint32_t raw[64];
         {
           uint32_t(&r0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&raw[0]);
           uint32_t(&r1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&raw[32]);
-          tmem_ld32(at, r0);
-          tmem_ld32(at + 32, r1);
+          tmem_ld32(at_s, r0);
+          tmem_ld32(at_s + 32, r1);
           tmem_wait_ld_fence(r0);
           tmem_wait_ld_fence(r1);
         }
@@ -615,7 +619,12 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
         // O's row is rescaled once the maximum has grown by more than 2^8
         const bool grow = high > m + kRescale;
         const bool rescale = grow && m != -INFINITY;
-        if (__any_sync(0xffffffffu, rescale)) {  // O is at rest: see the products' order
+        if (__any_sync(0xffffffffu, rescale)) {
+          // (a maximum that grows is not the part's first: t > 0)
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_done[tile][(n - 1) & 1], ((n - 1) >> 1) & 1,
+                                                 abort, A.status));
+          if (!ok) break;
+          tc_fence_after();
           const float shrink = rescale ? ex2_approx(m - high) : 1.f;
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
@@ -655,17 +664,18 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
         float s0, s1;
         unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
         l += s0 + s1;
-        tmem_st32(at, pk);
+        tmem_st32(at_s, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.p_full[tile]);
+        if (lane == 0) mbar_arrive(&bars.p_full[tile][n & 1]);
       }
       if (!ok && lane == 0) give_up();
       // ---- epilogue
       if (ok && steps > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_final[tile], ended & 1, abort, A.status));
-        ++ended;
+        const uint32_t n = gt[tile] + steps - 1;
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(&bars.o_done[tile][n & 1], (n >> 1) & 1, abort, A.status));
         if (!ok && lane == 0) give_up();
       }
       tc_fence_after();
