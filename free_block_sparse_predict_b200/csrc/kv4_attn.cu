@@ -729,9 +729,11 @@ struct Plan {
 };
 
 // More rows than this per request and KV head (tokens times the group's heads)
-// are a piece of a prompt, kv4_piece.cu: there a key costs a SM 10 to 20 clocks
-// for up to 256 rows, here some 10 for every 16.
-constexpr int64_t kFewRows = 32;
+// are a piece of a prompt, kv4_piece.cu, whose steps cost about the same for up
+// to 256 rows, while here every 16 rows read the codes again.  16 requests of up
+// to 32,768 keys, 8 KV heads of 128 channels, here and there: 338 and 405 us for
+// 48 rows, 445 and 457 for 64, 632 and 448 for 96, 1598 and 569 for 256.
+constexpr int64_t kFewRows = 64;
 
 // CTAs from the bounds that the host knows (lengths are on the device): all
 // that are resident at once, fewer when there cannot be a step for each warp.
@@ -750,7 +752,7 @@ Plan make_plan(const sparge_kv4_t& c, const sparge_kv4_attn_t& a) {
   Plan p{};
   int64_t rows = int64_t(a.max_q) * (a.Hq / c.Hkv);
   if (rows > kFewRows) {
-    // a unit's start costs twelve steps, so shorter lines take no more CTAs
+    // a unit's start costs eight steps, so shorter lines take no more CTAs
     p.piece_grid = grid_of(c, a, cdiv(rows, kPieceRows), 64, kSms, 1);
     if (a.R == 1) return p;
     rows = kFewRows;  // the other requests may bring few

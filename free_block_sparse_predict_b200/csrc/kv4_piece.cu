@@ -7,14 +7,25 @@
 // per SM:
 //   warp 0       bulk copies of the step's four 16-token tiles of codes
 //   warp 1       tensor memory, and one thread that issues every tcgen05.mma:
-//                S = Q K^T (128 x 64), O += P V, for one tile while the other's
-//                softmax runs
+//                S = Q K^T (128 x 64), a step ahead of the softmax, and O += P V
 //   warps 4-7    codes to fp16: K and V rows of 128-byte-swizzled tiles
 //   warps 8-15   softmax, a thread per row: mask, running maximum, P in fp16
 //                over S, lazy rescale of O, the epilogue
-// Both products take A from tensor memory (Q, P): with Q in shared memory, read
-// again for every 64 keys, a product of S took 90 clocks, not 32.  K and V are
-// made once for both tiles.
+// K and V are made once for both tiles.  Tensor memory holds two S of 64 columns
+// and O per tile, so Q stays in shared memory: with Q in tensor memory and one S,
+// each step waited for the last one's products (658 us against 538 below).
+//
+// Two prompts' last 512 of 20,001 and 32,768 tokens, 32 heads of 128 channels over
+// 8, take 538 us: 4.4e11 floating-point operations at 0.81 PFLOP/s, 49 % of the
+// library's rate for large products.  A step takes 2,900 clocks, of which the products
+// fill 1,500 (those of S, with half the columns that the pipe can take, are half
+// of it); the softmax's 2,700 are the longest chain: 600 to load S and find its
+// maximum, 1,600 for weights, of which the 1,024 of the exponential unit are
+// shared by both tiles, and 400 from P to the next S.  Without the exponentials
+// it took 490 us, without the codes' conversion 517, without either and the
+// rest of the softmax's arithmetic 407.  Measured and not kept: the tiles taking turns at the
+// exponentials (604), two warps per row with a step each, 24 warps with 88
+// registers (720), polling without the barrier unit's suspension (725).
 //
 // Values: s c has 14 bits.  For bf16 outputs K and V are s c / 2 rounded to fp16
 // (half of the codes lose nothing; halved, the largest scale's fit).  fp16
@@ -30,6 +41,7 @@
 // the CTA that comes last, as in kv4_attn.cu.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "kv4_common.cuh"
 #include "kv4_layout.cuh"
@@ -52,8 +64,8 @@ constexpr int kKeys = 64;            // keys of a step
 constexpr int kFlags = 16;           // steps whose tiles' validity is remembered
 constexpr float kRescale = 8.0f;     // log2 units
 // A unit's start and end in steps: its queries, the pipeline's filling, the
-// epilogue (some 8 us against 0.6 us a step).
-constexpr int kUnitSteps = 12;
+// epilogue (some 12 us against 1.5 us a step; 5 to 10 measured the same).
+constexpr int kUnitSteps = 8;
 
 template <int D, int NG, bool SPLIT>
 struct PieceCfg {
@@ -352,23 +364,28 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
             }
             mma_commit(&bars.o_done[i][m & 1]);
           };
-          auto all_scores = [&](int t) {
+          auto keys_there = [&](int t) {
             const uint32_t n = g + t;
             if (!mbar_wait(&bars.k_full[n & 1], (n >> 1) & 1, abort, A.status)) return false;
             tc_fence_after();
-            for (int i = 0; i < tiles; ++i) scores(i, t);
-            mma_commit(&bars.k_empty[n & 1]);
             return true;
           };
           // S of the next step comes before P V of this one, so that the softmax need
           // not wait for it; its columns were those of P two steps back, whose P V has
-          // been issued before it.
-          if (ok && p.n > 0) ok = all_scores(0);
+          // been issued before it.  The order S0, P V0, S1, P V1 of the tiles took 4 %
+          // less time than both S before both P V.
+          if (ok && p.n > 0 && (ok = keys_there(0))) {
+            for (int i = 0; i < tiles; ++i) scores(i, 0);
+            mma_commit(&bars.k_empty[g & 1]);
+          }
           for (int t = 0; t < p.n && ok; ++t) {
             const uint32_t n = g + t, b = n & 1;
-            if (t + 1 < p.n && !(ok = all_scores(t + 1))) break;
-            for (int i = 0; i < tiles && ok; ++i) {
+            const bool more = t + 1 < p.n;
+            if (more && !(ok = keys_there(t + 1))) break;
+            for (int i = 0; i < tiles; ++i) {
               const uint32_t m = gt[i] + t;
+              if (more) scores(i, t + 1);
+              if (more && i + 1 == tiles) mma_commit(&bars.k_empty[b ^ 1]);
               ok = mbar_wait(&bars.p_full[i][m & 1], (m >> 1) & 1, abort, A.status) &&
                    (i > 0 || mbar_wait(&bars.v_full[b], (n >> 1) & 1, abort, A.status));
               if (!ok) break;
@@ -643,24 +660,24 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
         const uint64_t f2 = pack2(f, f), nb2 = pack2(nb, nb);
         uint32_t pk[32];
         uint64_t sum[4] = {0, 0, 0, 0};
+        // (two copies: with the choice inside, the exponentials of all keys come
+        // before the first sum)
+        const auto weigh = [&](auto some_masked) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          float y0, y1;
-          unpack2(fma2(pack2(__uint_as_float(raw[c]), __uint_as_float(raw[c + 1])), f2, nb2), y0, y1);
-          raw[c] = __float_as_uint(ex2_approx(y0));
-          raw[c + 1] = __float_as_uint(ex2_approx(y1));
-        }
-        if (masked) {  // (-inf times f is a NaN where f is 0)
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (!(vis[c >> 5] >> (c & 31) & 1u)) raw[c] = 0u;
-        }
-#pragma unroll
-        for (int c = 0; c < 64; c += 2) {
-          const float y0 = __uint_as_float(raw[c]), y1 = __uint_as_float(raw[c + 1]);
-          sum[(c >> 1) & 3] = add2(sum[(c >> 1) & 3], pack2(y0, y1));
-          pk[c / 2] = pack_half2(y0, y1);
-        }
+          for (int c = 0; c < 64; c += 2) {
+            float y0, y1;
+            unpack2(fma2(pack2(__uint_as_float(raw[c]), __uint_as_float(raw[c + 1])), f2, nb2), y0, y1);
+            y0 = ex2_approx(y0);
+            y1 = ex2_approx(y1);
+            if constexpr (some_masked) {  // (-inf times f is a NaN where f is 0)
+              if (!(vis[c >> 5] >> (c & 31) & 1u)) y0 = 0.f;
+              if (!(vis[c >> 5] >> ((c & 31) + 1) & 1u)) y1 = 0.f;
+            }
+            sum[(c >> 1) & 3] = add2(sum[(c >> 1) & 3], pack2(y0, y1));
+            pk[c / 2] = pack_half2(y0, y1);
+          }
+        };
+        if (masked) weigh(std::true_type{}); else weigh(std::false_type{});
         float s0, s1;
         unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
         l += s0 + s1;

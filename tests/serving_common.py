@@ -218,7 +218,7 @@ class AttnCase:
     def exact(self, causal=True, scale=None):
         """(o, lse, size, err, keys, round, many): float64; per row sum_n p_n |v_n|, the E of its
         scores (see check_attn), the number of its keys, scale max_n sum |q||k_n| where K is
-        rounded, and whether its request has more than 32 rows for a KV head."""
+        rounded, and whether its request has more than 64 rows for a KV head."""
         T, Hq, d = self.q.shape
         Hkv = self.c.Hkv
         scale = d ** -0.5 if scale is None else scale
@@ -249,7 +249,7 @@ class AttnCase:
                 err[row:row + m] = torch.where(see[:, None], big, torch.zeros_like(big)).amax(-1)
                 mass = torch.einsum("ihd,nhd->ihn", q.abs(), k.abs()) * scale
                 sums[row:row + m] = torch.where(see[:, None], mass, torch.zeros_like(mass)).amax(-1)
-            many[row:row + m] = m * (Hq // Hkv) > 32
+            many[row:row + m] = m * (Hq // Hkv) > 64
             at, row = at + n, row + m
         return o, lse, size, err, keys, sums * many * (self.q.dtype is torch.bfloat16), many
 
@@ -266,7 +266,7 @@ def check_attn(case, got, want):
     6 standard deviations of n independent ones.  Sums of up to max |v| in n/64 (at most 512) steps a warp, each off by
     2^-22 of them.  Then the output's rounding.
 
-    Requests with more than 32 rows for a KV head: sums of n/64 steps (any number), and in
+    Requests with more than 64 rows for a KV head: sums of n/64 steps (any number), and in
     bf16 the values of K and V are rounded to fp16 first: 2^-11 of each, so scores are off by up
     to 2^-11 scale max_n sum |q||k_n| more and o by 2^-11 sum p |v|; P up to 2^8 is rounded
     once.  In fp16 K and V are sums of exact parts."""

@@ -232,8 +232,8 @@ def test_binding_refusals():
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("d,group", SHAPES)
 @pytest.mark.parametrize("lens,news,Hq,Hkv", [
-    ([33], [33], 1, 1), ([129, 64, 300], [129, 17, 257], 4, 2), ([2000, 63, 700, 5], [40, 1, 300, 5], 8, 1),
-    ([9000], [70], 6, 2), ([1500, 1400], [513, 64], 5, 5)])
+    ([33], [33], 1, 1), ([64], [64], 1, 1), ([65], [65], 1, 1), ([1100], [1100], 1, 1),
+    ([129, 64, 300], [129, 17, 257], 4, 2), ([2000, 63, 700, 5], [40, 1, 300, 5], 8, 1), ([9000], [70], 6, 2), ([1500, 1400], [513, 64], 5, 5)])
 def test_pieces_of_prompts(lens, news, Hq, Hkv, d, group, dtype):
     """Many rows per request: one and two tiles of 128 rows, part tiles, units cut over CTAs, and
     requests with few rows in the same call."""
