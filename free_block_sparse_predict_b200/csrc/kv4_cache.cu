@@ -31,9 +31,20 @@ constexpr int kCacheThreads = 256;
 // Largest scale kept: a softmax weight of up to 4 times it stays below 65504.
 constexpr float kMaxScale = 16376.0f;
 
-__device__ __forceinline__ float max_nan(float a, float b) {
+// The larger magnitudes of two pairs, with some sign; a NaN where either is one.
+template <int DT>
+__device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if (DT == SPARGE_BF16)
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Within 2^-23 of 1 / x, relatively.
+__device__ __forceinline__ float rcp_approx(float x) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -150,14 +161,13 @@ __global__ void __launch_bounds__(kCacheThreads) append_kernel(const CacheArgs A
         x[2 * i + 1] = f.y;
       }
     }
-    float m = 0.f;
+    uint32_t big = max_abs<DT>(max_abs<DT>(u[0], u[1]), max_abs<DT>(u[2], u[3]));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(x[i]));
-#pragma unroll
-    for (int o = 1; o < GL; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-    // s = fp16(m / 7) and codes rint(x / s), the quotients correctly rounded by
-    // Markstein's step from a correctly rounded reciprocal y: q = q0 + (a - q0 b) y
-    // with q0 = a y.  (IEEE divisions took three times all other instructions.)
+    for (int o = 1; o < GL; o <<= 1) big = max_abs<DT>(big, __shfl_xor_sync(0xffffffffu, big, o));
+    big = max_abs<DT>(big, big >> 16) & 0x7FFFu;
+    float m = DT == SPARGE_BF16 ? __uint_as_float(big << 16)
+                                : __half2float(__ushort_as_half(uint16_t(big)));
+    // s = fp16(m / 7), the quotient correctly rounded by Markstein's step.
     const bool high = m > 7.0f * kMaxScale;  // as m / 7 > kMaxScale: false for a NaN
     if (high) {
       m = 7.0f * kMaxScale;
@@ -174,14 +184,20 @@ __global__ void __launch_bounds__(kCacheThreads) append_kernel(const CacheArgs A
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = s > 0.f ? fminf(fmaxf(x[i], -most), most) : 0.f;
     }
-    const float y = s > 0.f ? __frcp_rn(s) : 0.f;
-    const uint64_t y2 = pack2(y, y), s2 = pack2(s > 0.f ? -s : 0.f, s > 0.f ? -s : 0.f);
-    // rounded to a whole number, plus 8, by the sum's own rounding: the low bits
+    // Codes are those of the correctly rounded quotient, without it: x and s have at
+    // most 11 bits and |x| < 8 s, so x / s is k + 1/2 or at least 2^-13 away from
+    // it.  Rounded to a multiple of 2^-16 (in the sum with 192), x y with a reciprocal good
+    // to 2^-22 falls on the halves exactly and on the right side elsewhere.  The
+    // next sum's rounding makes it a whole number, plus 8: the low bits.  (Markstein's step
+    // for each quotient took twice as many instructions, 80 instead of 76 us for
+    // three prompts in and back; IEEE divisions three times all the others.)
+    const float y = s > 0.f ? rcp_approx(s) : 0.f;
+    const uint64_t y2 = pack2(y, y), grid = pack2(192.0f, 192.0f);
     uint32_t c[4];  // two codes each, in the two half-words
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint64_t z = pack2(x[2 * i], x[2 * i + 1]), q0 = mul2(z, y2);
-      const uint64_t q = add2(fma2(fma2(q0, s2, z), y2, q0), pack2(12582920.0f, 12582920.0f));
+      const uint64_t q = add2(fma2(pack2(x[2 * i], x[2 * i + 1]), y2, grid),
+                              pack2(12582920.0f - 192.0f, 12582920.0f - 192.0f));
       c[i] = __byte_perm(uint32_t(q), uint32_t(q >> 32), 0x5410);
     }
     if (!is_v) {

@@ -1,7 +1,6 @@
 // extern "C" entry points around the prompt pass: argument validation and
 // launches of the rotary-position, paging and 4-bit-cache kernels on the
 // caller's stream.  See include/sparge.h.
-#include <cmath>
 #include <cstdint>
 
 #include "sparge_internal.h"
@@ -91,7 +90,7 @@ sparge_status_t check_attn(const sparge_kv4_t* c, const sparge_kv4_attn_t* a) {
   if (st != SPARGE_OK) return st;
   if (a == nullptr || a->R < 0 || a->T < 0 || a->Hq < 1 || a->Hq % c->Hkv != 0 || a->max_q < 0 ||
       a->max_pages < 0 || a->max_len < 0 || (a->causal != 0 && a->causal != 1) ||
-      !std::isfinite(a->scale) || !(a->scale > 0.f) ||
+      !(a->scale > 0.f) || !(a->scale <= 0x1p100f) ||
       (a->dtype != SPARGE_F16 && a->dtype != SPARGE_BF16))
     return SPARGE_EINVAL;
   if (a->T > 1 && (a->q_stride < int64_t(a->Hq) * c->d || a->q_stride > (int64_t(1) << 40)))

@@ -339,7 +339,7 @@ typedef struct {
   int32_t max_pages;      /* width of the block table                                      */
   int32_t max_len;        /* no request is longer; 0: max_pages * page_size                */
   int32_t causal;         /* 1: a token sees the keys up to its own; 0: all of its request */
-  float scale;            /* score scale, normally 1/sqrt(d)                               */
+  float scale;            /* score scale in (0, 2^100], normally 1/sqrt(d)                 */
   sparge_dtype_t dtype;   /* of q and o: SPARGE_F16 or SPARGE_BF16                         */
   int64_t q_stride;       /* elements between tokens of q, heads are d apart               */
 } sparge_kv4_attn_t;
@@ -359,6 +359,10 @@ size_t sparge_kv4_workspace_bytes(const sparge_kv4_t* c, const sparge_kv4_attn_t
  *   o    [T, Hq, d] of dtype; lse: nullable float32 [T, Hq], log of the sum of exponentials
  * Q is taken to fp16 with one power of two per row, products accumulate in float32, softmax
  * statistics are float32; a weight, and its product with V's scale, are rounded to fp16.
+ * Requests with more than 64 rows for a KV head (new tokens times Hq / Hkv; of a call's only
+ * request, max_q tokens) go through tiles of K and V in fp16: there the values c * s are taken
+ * as they are for fp16 rows and rounded to fp16 (by up to 2^-11 of each) for bf16 rows, and a
+ * NaN scale of V makes every channel NaN in the rows that see its token, not its group's alone.
  * Keys at pages outside [0, num_pages) or behind max_len are left out; these, a length below
  * 0 and a cu_q that does not ascend within [0, T] by steps of at most max_q (such a request
  * is skipped) put SPARGE_EINVAL into the workspace's status word (sparge_device_status).
@@ -369,8 +373,9 @@ sparge_status_t sparge_kv4_attn(const sparge_kv4_t* c, const sparge_kv4_attn_t* 
                                 float* lse, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* Synchronises the stream and returns the status word that kernels write to
- * the workspace (SPARGE_OK, SPARGE_ETIMEOUT or SPARGE_ERANGE), then clears it.
- * ws: the workspace of sparge_predict_mask / sparge_attn_fwd. */
+ * the workspace (SPARGE_OK, SPARGE_ETIMEOUT, SPARGE_ERANGE or, from sparge_kv4_attn,
+ * SPARGE_EINVAL), then clears it.
+ * ws: the workspace of sparge_predict_mask / sparge_attn_fwd, or of sparge_kv4_attn. */
 sparge_status_t sparge_device_status(void* ws, cudaStream_t stream);
 
 /* Failure-detection self-test (no counterpart in the paper): launches one

@@ -222,7 +222,7 @@ def test_binding_refusals():
            dict(o=o[:1]), dict(o=o.bfloat16()), dict(o=o.cpu()), dict(block_table=case.table[0]),
            dict(block_table=case.table.long()), dict(block_table=case.table.t()), dict(seq_len=case.lens_t[:1]),
            dict(cu_q=case.cu[:2]), dict(cu_q=case.cu.long()), dict(ws=case.ws[:64]), dict(cache=case.cache[:1]),
-           dict(scale=0.0), dict(scale=float("nan")), dict(max_q=-1), dict(lse=o), dict(ws=case.ws.cpu()),
+           dict(scale=0.0), dict(scale=float("nan")), dict(scale=1e31), dict(max_q=-1), dict(lse=o), dict(ws=case.ws.cpu()),
            dict(q=case.q[:, :3], o=o[:, :3].contiguous()), dict(o=case.q.contiguous(), q=case.q.contiguous().view(2, 4, 64)[:, :4], seq_len=case.cu[:1])]
     for kw in bad:
         with pytest.raises(fb.SpargeError):

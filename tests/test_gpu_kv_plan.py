@@ -84,13 +84,14 @@ def test_nothing():
     run((np.array([1, -1]), np.array([0, 0]), np.zeros((2, 0), np.int64), z, 0, 16), 3)
 
 
-def test_replayed_graph_advances_its_state():
+@pytest.mark.parametrize("slots", [50, 40_000])   # one cluster of CTAs, a whole grid
+def test_replayed_graph_advances_its_state(slots):
     """Captured in place, the step decodes by itself: each replay is the definition's next step."""
     rng = np.random.default_rng(5)
     new, length, table, free, count, P = random_plan(rng, 40, 16, 12, 1, ended=0.0, idle=0.2)
     length = length // 2
     args = (new, length, table, free, count, P)
-    s = PlanState(*args, 50, dev(), in_place=True)
+    s = PlanState(*args, slots, dev(), in_place=True)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     g = torch.cuda.CUDAGraph()
@@ -98,7 +99,7 @@ def test_replayed_graph_advances_its_state():
         s.call(fb)
     for _ in range(20):
         g.replay()
-        want = plan_oracle(new, length, table, free, count, P, 50)
+        want = plan_oracle(new, length, table, free, count, P, slots)
         torch.cuda.synchronize()
         same(s.outputs(), want)
         length, table, free, count = want["length"], want["table"], want["free"], want["count"]

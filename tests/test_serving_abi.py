@@ -222,7 +222,8 @@ def _attn_call(native, c, a, ws_bytes=1 << 30, **swap):
 @pytest.mark.parametrize("kw,code", [
     (dict(R=-1), 1), (dict(T=-1), 1), (dict(Hq=0), 1), (dict(Hq=5), 1), (dict(max_q=-1), 1),
     (dict(max_pages=-1), 1), (dict(max_len=-1), 1), (dict(causal=2), 1), (dict(scale=0.0), 1),
-    (dict(scale=float("inf")), 1), (dict(dtype=2), 1), (dict(q_stride=128), 1), (dict(q_stride=260), 2),
+    (dict(scale=float("inf")), 1), (dict(scale=1e31), 1), (dict(dtype=2), 1),
+    (dict(q_stride=128), 1), (dict(q_stride=260), 2),
     (dict(R=70000), 2), (dict(max_pages=1 << 27), 2), (dict(T=1 << 30), 2),
     (dict(max_q=1 << 30), 2)])
 def test_attention_parameters_refused(native, kw, code):
