@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kCacheThreads) append_kernel(const CacheArgs A
     // it.  Rounded to a multiple of 2^-16 (in the sum with 192), x y with a reciprocal good
     // to 2^-22 falls on the halves exactly and on the right side elsewhere.  The
     // next sum's rounding makes it a whole number, plus 8: the low bits.  (Markstein's step
-    // for each quotient took twice as many instructions, 80 instead of 76 us for
+    // for each quotient took twice as many instructions, 80.4 instead of 76.4 us for
     // three prompts in and back; IEEE divisions three times all the others.)
     const float y = s > 0.f ? rcp_approx(s) : 0.f;
     const uint64_t y2 = pack2(y, y), grid = pack2(192.0f, 192.0f);
