@@ -1,4 +1,5 @@
-"""Builds libsparge.so (the C-ABI CUDA library) in-tree for sm_100a.
+"""Builds libsparge.so (the C-ABI CUDA library, for sm_100a) and _serving.so (the argument
+checks of serving.py's calls, host C++) in-tree.
 
     python -m free_block_sparse_predict_b200.build
 
@@ -10,10 +11,12 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsparge.so")
+BINDING = os.path.join(PKG, "_serving.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -53,11 +57,31 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def _binding() -> None:
+    src = os.path.join(CSRC, "serving_binding.cpp")
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "sparge.h")))
+    if os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    inc = os.path.join(torch, "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    dirs = [INCLUDE, inc, os.path.join(inc, "torch", "csrc", "api", "include"),
+            sysconfig.get_paths()["include"], cuda]
+    cmd = ["g++", "-shared", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", src, "-o", BINDING]
+    cmd += [x for d in dirs for x in ("-isystem" if d != INCLUDE else "-I", d)]
+    cmd += ["-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+
+
 def build(extra=(), verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        binding = ex.submit(_binding)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
+        binding.result()
     newest = max(os.path.getmtime(o) for o in objs)
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < newest:
         cmd = [nvcc(), "-shared", "-o", LIB] + objs + ARCH

@@ -247,3 +247,23 @@ def test_attention_pointers_and_workspace(native):
     assert _attn_call(native, c, a, ws=FAR[1]) == 1               # inside the cache
     for kw in (dict(R=0), dict(T=0), dict(max_q=0)):
         assert _attn_call(native, c, _attn(native, **kw), q=None, o=None) == 0
+
+
+def test_binding_refuses_before_the_library_is_called():
+    """Host tensors, things that are no tensors, a cache without a shape: SpargeError each."""
+    import free_block_sparse_predict_b200 as fb
+    i, f = torch.zeros(4, dtype=torch.int32), torch.zeros(2, dtype=torch.float64)
+    x = torch.zeros(1, 2, 4, 64)
+    c, rows = fb.make_kv4(2, 64, 32, 16, 1), torch.zeros(4, 2, 64)
+    memory, table = torch.zeros(4096, dtype=torch.uint8), torch.zeros(4, 1, dtype=torch.int32)
+    calls = [lambda t: fb.sparge_rope_apply(t, x, i[None], f, i[:2]),
+             lambda t: fb.sparge_rope_inverse(x, t, i[None], f, i[:2]),
+             lambda t: fb.sparge_kv_plan(i, i, table, i, i, 16, i, i, t, i, i),
+             lambda t: fb.sparge_kv4_append(c, rows, rows, i, t),
+             lambda t: fb.sparge_kv4_read(c, t, i, rows, rows),
+             lambda t: fb.sparge_kv4_attn(c, t, memory, table, i, i, 1, rows, memory)]
+    for call in calls:
+        for t in (x, None, 3):
+            with pytest.raises(fb.SpargeError) as e:
+                call(t)
+            assert e.value.code == 1
