@@ -42,6 +42,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "after.cuh"
 #include "kv4_common.cuh"
 #include "kv4_layout.cuh"
 #include "sm100_ptx.cuh"
@@ -168,6 +169,8 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
     fence_async_shared();
   }
 
+  begin_after();
+
   // ---- the line of units: its length, and the request where this part starts
   const int per = (A.R + kAttnThreads - 1) / kAttnThreads;
   const int r_lo = min(A.R, int(threadIdx.x) * per), r_hi = min(A.R, r_lo + per);
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
       const int i = BATCH_STEPS * batch + lane / TPS;
       const int ti = TPS * (step0 + warp + kWarps * i) + lane % TPS;
       if (i >= mine || ti >= n_tiles) return -1;
-      const int32_t entry = A.tpp.quot(ti), page = __ldg(table + entry);
+      const int32_t entry = A.tpp.quot(ti), page = table[entry];
       if (uint32_t(page) >= uint32_t(A.num_pages)) {
         atomicCAS(A.status, 0, int32_t(SPARGE_EINVAL));
         return -1;
@@ -777,8 +780,8 @@ cudaError_t run(const DecodeArgs& a, const Plan& p, cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute(
       kv4_attn_kernel<D, NG, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  kv4_attn_kernel<D, NG, NT><<<unsigned(p.grid), kAttnThreads, C::SMEM, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(kv4_attn_kernel<D, NG, NT>, dim3(unsigned(p.grid)), kAttnThreads, C::SMEM,
+                      stream, a);
 }
 
 template <int D, int NG>

@@ -19,6 +19,7 @@
 
 #include <cstdint>
 
+#include "after.cuh"
 #include "kv4_layout.cuh"
 #include "sm100_ptx.cuh"
 #include "sparge_internal.h"
@@ -107,6 +108,7 @@ __global__ void __launch_bounds__(kCacheThreads) append_kernel(const CacheArgs A
   __shared__ uint32_t s_v[C::HEADS][WORDS][PITCH];
   __shared__ __align__(16) __half s_scale[C::HEADS][kRows][2 * NG];
 
+  begin_after();
   const int32_t row0 = int32_t(blockIdx.x) * kRows, head0 = int32_t(blockIdx.y) * C::HEADS;
   const bool is_v = threadIdx.x / 32 & 1;
   const int lane = threadIdx.x % LANES;
@@ -241,6 +243,7 @@ __global__ void __launch_bounds__(kCacheThreads) read_kernel(const CacheArgs A) 
   constexpr Kv4Tile L{D, NG};
   __shared__ int32_t s_slot[kRows];
   __shared__ int64_t s_tile[kRows];
+  begin_after();
   const int32_t row0 = int32_t(blockIdx.x) * kRows, head0 = int32_t(blockIdx.y) * C::HEADS;
   const bool is_v = threadIdx.x / 32 & 1;
   const int lane = threadIdx.x % LANES;
@@ -327,8 +330,7 @@ template <bool READ, int D, int NG>
 cudaError_t run(const CacheArgs& a, cudaStream_t stream) {
   const dim3 grid(unsigned(cdiv(a.T, kRows)), unsigned(cdiv(a.Hkv, CacheCfg<D>::HEADS)));
   const auto go = [&](auto* kernel) {
-    kernel<<<grid, kCacheThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(kernel, grid, kCacheThreads, 0, stream, a);
   };
   if (a.dtype == SPARGE_F16)
     return READ ? go(read_kernel<D, NG, SPARGE_F16>) : go(append_kernel<D, NG, SPARGE_F16>);

@@ -43,6 +43,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "after.cuh"
 #include "kv4_common.cuh"
 #include "kv4_layout.cuh"
 
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
   __shared__ int s_abort, s_last;
   __shared__ uint32_t s_valid[kFlags];    // bit u: tile u of the step was copied
   __shared__ uint32_t s_nan[kFlags][2];   // keys whose V has a NaN scale
+  begin_after();
   if (smem_u32(smem) & 1023u) {  // the swizzle counts from 1024-byte boundaries
     if (threadIdx.x == 0) atomicCAS(A.status, 0, int32_t(SPARGE_EUNSUPPORTED));
     return;
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
             const int ti = 4 * (p.step0 + t) + lane;
             id = -1;
             if (ti < p.n_tiles) {
-              const int32_t entry = A.tpp.quot(ti), page = __ldg(table + entry);
+              const int32_t entry = A.tpp.quot(ti), page = table[entry];
               if (uint32_t(page) < uint32_t(A.num_pages))
                 id = (page * A.Hkv + p.kvh - entry) * int32_t(A.tpp.d) + ti;
               else
@@ -805,8 +807,8 @@ cudaError_t run_one(const DecodeArgs& a, int grid, cudaStream_t stream) {
   const cudaError_t f = cudaFuncGetAttributes(&fa, kv4_piece_kernel<D, NG, SPLIT>);
   if (f != cudaSuccess) return f;
   if (fa.numRegs != kLaunchRegs) return cudaErrorNotSupported;
-  kv4_piece_kernel<D, NG, SPLIT><<<unsigned(grid), kPieceThreads, C::SMEM, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(kv4_piece_kernel<D, NG, SPLIT>, dim3(unsigned(grid)), kPieceThreads, C::SMEM,
+                      stream, a);
 }
 
 template <int D, int NG>

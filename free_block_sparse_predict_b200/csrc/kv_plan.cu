@@ -19,6 +19,7 @@
 
 #include <cstdint>
 
+#include "after.cuh"
 #include "div.cuh"
 #include "sparge_internal.h"
 
@@ -82,6 +83,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
   int32_t* s_cu = s_dyn;             // [R + 1] start of each request's tokens
   int32_t* s_len = s_cu + A.R + 1;   // [R] L; -1: no tokens or not admitted; -2 - L: ended
   int32_t* s_off = s_len + A.R;      // [R] pages pushed (ended) or popped before it
+
+  begin_after();
 
   const int32_t P = A.page_size;
   const int64_t cap = int64_t(A.max_pages) * P;
@@ -281,7 +284,7 @@ cudaError_t run(const KvPlanArgs& a, int max_ctas, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   if (GRID) {
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
@@ -289,9 +292,11 @@ cudaError_t run(const KvPlanArgs& a, int max_ctas, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = unsigned(n);
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
   }
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = GRID ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, kernel, a, make_div(uint32_t(a.page_size)));
 }
 

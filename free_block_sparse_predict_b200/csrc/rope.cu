@@ -17,6 +17,7 @@
 
 #include <cstdint>
 
+#include "after.cuh"
 #include "sparge_internal.h"
 
 namespace sparge {
@@ -126,11 +127,12 @@ template <int DT, bool IL>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const RopeArgs P) {
   using T = RopeType<DT>;
   constexpr int V = T::V;
+  begin_after();
   const int64_t item = int64_t(blockIdx.x) * kRopeThreads + threadIdx.x;
   const int32_t p = int32_t(item / P.units);
   const int32_t u = int32_t(item - int64_t(p) * P.units);
   if (p >= P.N) return;
-  const int32_t s = P.perm == nullptr ? p : __ldg(P.perm + p);
+  const int32_t s = P.perm == nullptr ? p : P.perm[p];
   if (uint32_t(s) >= uint32_t(P.N)) return;
 
   // the two vectors of this thread; vectors behind the turned ones are copied
@@ -170,11 +172,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const Rop
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const int32_t pair = u * V + k;
-        const int32_t ax = __ldg(P.axis + pair);
+        const int32_t ax = P.axis[pair];
         const double at =
-            uint32_t(ax) < uint32_t(P.axes) ? double(__ldg(pos + int64_t(ax) * P.N + s)) : 0.0;
+            uint32_t(ax) < uint32_t(P.axes) ? double(pos[int64_t(ax) * P.N + s]) : 0.0;
         // 1 / (2 pi): turns, then the nearest whole turn off
-        const double t = at * (__ldg(P.inv_freq + pair) * 0.15915494309189535);
+        const double t = at * (P.inv_freq[pair] * 0.15915494309189535);
         const float f = float(2.0 * (t - rint(t)));
         sincospif(f, &sn[k], &cs[k]);
         if (P.inverse) sn[k] = -sn[k];
@@ -229,23 +231,24 @@ cudaError_t launch_rope(const sparge_rope_t& p, const void* src, const int64_t* 
   a.groups = int32_t(cdiv(p.H, a.heads));
   const int64_t gy = int64_t(p.B) * a.groups;
   const dim3 grid{unsigned(gx), unsigned(gy < 65535 ? gy : 65535), 1u};
+  cudaError_t e;
   if (p.dtype == SPARGE_F16) {
     if (p.interleaved)
-      rope_kernel<SPARGE_F16, true><<<grid, kRopeThreads, 0, stream>>>(a);
+      e = launch_after(rope_kernel<SPARGE_F16, true>, grid, kRopeThreads, 0, stream, a);
     else
-      rope_kernel<SPARGE_F16, false><<<grid, kRopeThreads, 0, stream>>>(a);
+      e = launch_after(rope_kernel<SPARGE_F16, false>, grid, kRopeThreads, 0, stream, a);
   } else if (p.dtype == SPARGE_BF16) {
     if (p.interleaved)
-      rope_kernel<SPARGE_BF16, true><<<grid, kRopeThreads, 0, stream>>>(a);
+      e = launch_after(rope_kernel<SPARGE_BF16, true>, grid, kRopeThreads, 0, stream, a);
     else
-      rope_kernel<SPARGE_BF16, false><<<grid, kRopeThreads, 0, stream>>>(a);
+      e = launch_after(rope_kernel<SPARGE_BF16, false>, grid, kRopeThreads, 0, stream, a);
   } else {
     if (p.interleaved)
-      rope_kernel<SPARGE_F32, true><<<grid, kRopeThreads, 0, stream>>>(a);
+      e = launch_after(rope_kernel<SPARGE_F32, true>, grid, kRopeThreads, 0, stream, a);
     else
-      rope_kernel<SPARGE_F32, false><<<grid, kRopeThreads, 0, stream>>>(a);
+      e = launch_after(rope_kernel<SPARGE_F32, false>, grid, kRopeThreads, 0, stream, a);
   }
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace sparge
