@@ -172,3 +172,57 @@ def test_prompt_by_the_sparse_pass_and_by_the_cache():
         want = exact.attend(0, now[t, :HQ], t + 1)
         # fp16 weights and values (2^-11 each) of up to |v| < 8, and the output's rounding
         assert np.all(np.abs(got[t] - want) <= 2.0 ** -9 * 8 + 2.0 ** -8 * np.abs(want))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_in_a_row_wait_for_one_another(captured):
+    """Launches begin before the one ahead of them has ended: steps that follow one another without
+    a pause, each reading what the calls before it wrote (tables, cache, its own output as the next
+    queries), give the bits of the same steps with a wait after every call."""
+    def run(pause):
+        torch.manual_seed(5)
+        R, tokens = 40, 3000
+        s = Server(R, 40, 1400, tokens)
+        s.free.copy_(torch.arange(1400, dtype=torch.int32))
+        s.pos.random_(0, 1000)
+        s.qkv.normal_()
+        names = ["sparge_rope_apply", "sparge_kv_plan", "sparge_kv4_append", "sparge_kv4_read",
+                 "sparge_kv4_attn"]
+        kept = {n: getattr(fb, n) for n in names}
+
+        def waiting(f):
+            def call(*a, **kw):
+                f(*a, **kw)
+                torch.cuda.synchronize()
+            return call
+
+        def steps():
+            for max_q, n in ((70, 1), (1, 50)):
+                s.new.fill_(max_q)
+                for _ in range(n):
+                    s.step(max_q)
+                    fb.sparge_kv4_read(s.c, s.cache, s.slots, s.qkv[:, HQ:HQ + HKV],
+                                       s.qkv[:, HQ + HKV:])
+                    s.qkv[:, :HQ].copy_(s.o)
+
+        if pause:
+            for n in names:
+                setattr(fb, n, waiting(kept[n]))
+        try:
+            torch.cuda.synchronize()
+            if captured and not pause:
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph, stream=torch.cuda.Stream(), capture_error_mode="relaxed"):
+                    steps()
+                graph.replay()
+            else:
+                steps()
+        finally:
+            for n in names:
+                setattr(fb, n, kept[n])
+        torch.cuda.synchronize()
+        assert fb.sparge_device_status(s.ws) == 0
+        return s.o, s.qkv, s.table, s.length, s.count, s.slots
+
+    for a, b in zip(run(False), run(True)):
+        assert torch.equal(a, b)
