@@ -19,12 +19,21 @@
 //
 // Scales: S is summed per group in float32, S = sum_g s_g S_g.  V's scale
 // goes into the weights: p is rounded to fp16 and p s once more (the sum of
-// weights is of the unrounded p; both roundings are far below the 4 bits' own
-// and together about the output's, and save a tenth of the instructions).  Q is fp16 with one power
+// weights is of the unrounded p; the two roundings are 2^-10 of p s together, half of a
+// bf16 output's own, and save a tenth of the instructions).  Q is fp16 with one power
 // of two per row, so bf16 queries lose nothing above 2^-26 of the row's
 // largest.  The running maximum is lazy: it is raised (and O rescaled) when a
-// score passes it by more than 2 in log2 units, so weights stay below 4 and
-// p s below 65504.
+// score passes it by more than 2 in log2 units, so weights are at most 4.
+//
+// fp16 ends at 2^-24, and an answer may be carried by very many keys of small
+// weight or by small values.  So p is held times 2^10 and s times a power of two
+// that brings the largest scale a warp has met to [8, 16), which just keeps 4 p s
+// below 65504: a key has all its bits down to p = 2^-24 and p s = 2^-27 of the
+// largest, whatever the size of V.  The power falls when a larger scale comes, with O, in
+// the branch of the maximum; a step's scales are looked over a lane a token.  All of it
+// costs 1 to 2 % (84.7 against 83.2 us for three requests of 115,000 keys).  Without it answers
+// that keys 14 nats below the largest carry were off by 58 % of sum p |v| where V was around 0.02,
+// with it by 0.2 %, a bf16 output's own rounding.
 //
 // Work is cut evenly, whatever the lengths: the units (request, KV head, tile
 // of 8 NT query rows) stand in one line, each as long as its keys in steps of
@@ -37,8 +46,8 @@
 // a ring of bulk copies of its own, and are joined in shared memory.
 //
 // Measured, 32 query heads of 128 channels over 8: one token of 48 requests of 700
-// to 8192 keys in 56.8 us (233 MB at 4.1 TB/s), of three of 115,000 in 83 us (396 MB
-// at 4.8 TB/s, 73 % of a copy's rate), of one of 1009 in 9 us.  Issue slots (60 to 65 %)
+// to 8192 keys in 57.5 us (233 MB at 4.1 TB/s), of three of 115,000 in 84.7 us (396 MB
+// at 4.7 TB/s, 71 % of a copy's rate), of one of 1009 in 9.2 us.  Issue slots (60 to 65 %)
 // and memory share the limit.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -62,6 +71,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kAttnThreads = kWarps * 32;
 constexpr float kLazy = 2.0f;      // log2 units
+constexpr int kLift = 10;          // log2 of what weights are held times
+constexpr int kTop = 4;            // V's scales are held below 2^kTop
+static_assert(kLazy + kLift + kTop == 16, "4 p s below 65504: 2^12 (16 - 2^-7)");
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -125,21 +137,30 @@ __device__ __forceinline__ void load_scales(const uint8_t* at, float (&x)[NG]) {
   }
 }
 
-// The same as fp16, each in both halves of a word.
+// Those of its V as they lie, two to a word (a single one alone).
 template <int NG>
-__device__ __forceinline__ void load_scales_twice(const uint8_t* at, uint32_t (&x)[NG]) {
+__device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&v)[(NG + 1) / 2]) {
   if constexpr (NG == 4) {
     const uint2 w = *reinterpret_cast<const uint2*>(at);
-    x[0] = __byte_perm(w.x, w.x, 0x1010), x[1] = __byte_perm(w.x, w.x, 0x3232);
-    x[2] = __byte_perm(w.y, w.y, 0x1010), x[3] = __byte_perm(w.y, w.y, 0x3232);
+    v[0] = w.x, v[1] = w.y;
   } else if constexpr (NG == 2) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(at);
-    x[0] = __byte_perm(w, w, 0x1010), x[1] = __byte_perm(w, w, 0x3232);
+    v[0] = *reinterpret_cast<const uint32_t*>(at);
   } else {
-    const uint32_t w = *reinterpret_cast<const uint16_t*>(at);
-    x[0] = __byte_perm(w, w, 0x1010);
+    v[0] = *reinterpret_cast<const uint16_t*>(at);
   }
 }
+// A pair of weights times the scale n of such words.
+__device__ __forceinline__ uint32_t times_scale(uint32_t p, const uint32_t* v, int n) {
+  const __half2 w = *reinterpret_cast<const __half2*>(&v[n / 2]);
+  const __half2 x = __hmul2_rn(*reinterpret_cast<const __half2*>(&p),
+                               n % 2 ? __high2half2(w) : __low2half2(w));
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+__device__ __forceinline__ float two_to(int n) { return __uint_as_float(uint32_t(n + 127) << 23); }
+// 2^n as fp16, -15 < n < 16, in both halves of a word, and back.
+__device__ __forceinline__ uint32_t half_two_to(int n) { return uint32_t(n + 15) * 0x04000400u; }
+__device__ __forceinline__ int half_log2(uint32_t x) { return int(x >> 26) - 15; }
 
 template <int D, int NG, int NT>
 __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
@@ -369,7 +390,6 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
       // since one may overflow
       const int field = int(__float_as_uint(big) >> 23);
       const int k = field < 255 ? 139 - field : 0, half_k = k >> 1;
-      const auto two_to = [](int n) { return __uint_as_float(uint32_t(n + 127) << 23); };
       const float k1 = two_to(half_k), k2 = two_to(k - half_k);
 #pragma unroll
       for (int j = 0; j < J; ++j)
@@ -394,6 +414,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
 
     float m[NT][2], l[NT][2];
     float o[NT][MT][4];
+    uint32_t s_lift = half_two_to(15);  // what V's scales are held times
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -473,7 +494,9 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[u][nt][c] *= f[nt][c & 1];
+            for (int c = 0; c < 4; c += 2)
+              unpack2(mul2(pack2(s[u][nt][c], s[u][nt][c + 1]), pack2(f[nt][0], f[nt][1])),
+                      s[u][nt][c], s[u][nt][c + 1]);
         }
         // ---- keys that a row does not see
         uint32_t seen = ~0u;  // bit 4 (NT u + nt) + c
@@ -491,9 +514,25 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
                 if (!yes) s[u][nt][c] = -INFINITY;
               }
         }
+        // ---- V's scales of the step, a lane a token: whether one times s_lift = 2^b is
+        // 2^kTop or more, that is, whether its bits reach those of 2^(kTop - b): the
+        // sum's top bit (a NaN's too)
+        auto scales = [&](uint32_t (&w)[(NG + 1) / 2]) {
+          load_words<NG>(tiles + (lane >> 4) * C::TILE + 16 * D + (lane & 15) * NG * 4 + 2 * NG, w);
+          // (of a token that does not exist any bytes may stand there)
+          if (MASKED && !((here >> (lane >> 4) & 1u) && key0 + lane < req.keys))
+            for (uint32_t& x : w) x = 0;
+        };
+        uint32_t over = 0;
+        {
+          uint32_t w[(NG + 1) / 2];
+          scales(w);
+#pragma unroll
+          for (uint32_t x : w) over |= x + (s_lift - (kTop - 2) * 0x04000400u);
+        }
         // ---- the running maximum
         float high[NT][2];  // this lane's largest of each column
-        bool raise = false;
+        bool raise = over & 0x80008000u;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -505,6 +544,18 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
             raise |= x > m[nt][c] + kLazy;
           }
         if (__any_sync(0xffffffffu, raise)) {
+          uint32_t w[(NG + 1) / 2], top = 0;
+          scales(w);  // again: seldom, and kept they would cost registers
+#pragma unroll
+          for (uint32_t x : w) {
+            const uint32_t lo = x & 0xFFFFu, hi = x >> 16;
+            if (lo < 0x7C00u) top = max(top, lo);  // (a NaN has no size)
+            if (hi < 0x7C00u) top = max(top, hi);
+          }
+          const uint32_t was = s_lift;
+          const int e = int(__reduce_max_sync(0xffffffffu, top) >> 10) - 15;
+          s_lift = min(s_lift, half_two_to(min(15, kTop - 1 - e)));
+          const float o_by = two_to(half_log2(s_lift) - half_log2(was));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -516,33 +567,44 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
               const float shrink = ex2_approx(m[nt][c] - now);
               m[nt][c] = now;
               l[nt][c] *= shrink;
+              const float by = shrink * o_by;
 #pragma unroll
-              for (int k = 0; k < MT; ++k) o[nt][k][c] *= shrink, o[nt][k][c + 2] *= shrink;
+              for (int k = 0; k < MT; ++k) o[nt][k][c] *= by, o[nt][k][c + 2] *= by;
             }
           }
         }
 #pragma unroll
         for (int u = 0; u < TPS; ++u) {
           const uint8_t* tile = tiles + u * C::TILE;
-          uint32_t sv[2][NG];  // of tokens g and g + 8, twice in a word
-          load_scales_twice<NG>(tile + 16 * D + g * NG * 4 + 2 * NG, sv[0]);
-          load_scales_twice<NG>(tile + 16 * D + (g + 8) * NG * 4 + 2 * NG, sv[1]);
+          uint32_t sv[2][(NG + 1) / 2];  // of tokens g and g + 8, lifted
+          load_words<NG>(tile + 16 * D + g * NG * 4 + 2 * NG, sv[0]);
+          load_words<NG>(tile + 16 * D + (g + 8) * NG * 4 + 2 * NG, sv[1]);
+#pragma unroll
+          for (int w = 0; w < (NG + 1) / 2; ++w)
+            sv[0][w] = times(sv[0][w], s_lift), sv[1][w] = times(sv[1][w], s_lift);
           // ---- weights, times V's scales, as B fragments (rows = keys)
           uint32_t pf[NT][NG][2];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float p[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              p[c] = ex2_approx(s[u][nt][c] - m[nt][c & 1]);
-              if (MASKED && !(seen >> (4 * (NT * u + nt) + c) & 1)) p[c] = 0.f;
+            // (two sums: the largest weight is a power of two exactly)
+            for (int c = 0; c < 4; c += 2) {
+              unpack2(add2(sub2(pack2(s[u][nt][c], s[u][nt][c + 1]), pack2(m[nt][0], m[nt][1])),
+                           pack2(kLift, kLift)),
+                      p[c], p[c + 1]);
+              p[c] = ex2_approx(p[c]);
+              p[c + 1] = ex2_approx(p[c + 1]);
             }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (MASKED && !(seen >> (4 * (NT * u + nt) + c) & 1)) p[c] = 0.f;
             l[nt][0] += p[0] + p[2];
             l[nt][1] += p[1] + p[3];
             const uint32_t pa = pack_half2(p[0], p[1]), pb = pack_half2(p[2], p[3]);
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-              uint32_t wa = times(pa, sv[0][n]), wb = times(pb, sv[1][n]);
+              uint32_t wa = times_scale(pa, sv[0], n), wb = times_scale(pb, sv[1], n);
               if (MASKED) {
                 // a key that is not seen counts nothing, whatever its scale is
                 const uint32_t bits = seen >> (4 * (NT * u + nt));
@@ -597,6 +659,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
 
     // ---- this warp's result: O[row][channel], maximum and sum
     float* so = reinterpret_cast<float*>(ring);
+    const float l_by = two_to(-kLift), o_by = two_to(-kLift - half_log2(s_lift));
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -604,11 +667,11 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], w);
         const int row = 8 * nt + 2 * t + c;
-        if (g == 0) s_ml[warp][row] = make_float2(m[nt][c], l[nt][c]);
+        if (g == 0) s_ml[warp][row] = make_float2(m[nt][c], l[nt][c] * l_by);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
           *reinterpret_cast<float2*>(so + row * C::PITCH + 16 * mt + 2 * g) =
-              make_float2(o[nt][mt][c], o[nt][mt][c + 2]);
+              make_float2(o[nt][mt][c] * o_by, o[nt][mt][c + 2] * o_by);
       }
     }
     __syncthreads();
