@@ -13,10 +13,10 @@
 //                over S, lazy rescale of O, the epilogue
 // K and V are made once for both tiles.  Tensor memory holds two S of 64 columns
 // and O per tile, so Q stays in shared memory: with Q in tensor memory and one S,
-// each step waited for the last one's products (658 us against 541 below).
+// each step waited for the last one's products (658 us).
 //
 // Two prompts' last 512 tokens against 52,000 keys together, 32 heads of 128
-// channels over 8, take 541 us: 4.4e11 floating-point operations at 0.81 PFLOP/s, 49 % of the
+// channels over 8, take 520 us: 4.4e11 floating-point operations at 0.84 PFLOP/s, 51 % of the
 // library's rate for large products.  A step takes 2,900 clocks, of which the products
 // fill 1,500 (those of S, with half the columns that the pipe can take, are half
 // of it); the softmax's 2,700 are the longest chain: 600 to load S and find its
@@ -27,11 +27,15 @@
 // exponentials (604), two warps per row with a step each, 24 warps with 88
 // registers (720), polling without the barrier unit's suspension (725).
 //
-// Values: s c has 14 bits.  For bf16 outputs K and V are s c / 2 rounded to fp16
-// (half of the codes lose nothing; halved, the largest scale's fit).  fp16
+// Values: s c has 14 bits.  For bf16 outputs K and V are s c rounded to fp16
+// (half of the codes lose nothing).  fp16
 // outputs show that (K's rounding alone is two and a half times their own), so
 // for them (SPLIT) K and V are each the sum of two tiles, the scale's upper
-// eight bits and the rest times c, both exact, with two products.  Q is fp16
+// eight bits and the rest times c, both exact, with two products.  A token of K or
+// of V with a scale of 8192 or more (7 s would pass fp16's end) has its row halved, and its
+// scores, or its weight in P, doubled: bits beside those of NaN scales tell the
+// softmax warps.  (All rows halved lost the last bit of scales below 2^-13, and 2^-24
+// itself.)  Q is fp16
 // with one power of two per row, P is fp16 of weights up to 2^8, sums are
 // float32.  A token whose scale of V is NaN makes the rows that see it NaN in
 // every channel: its row of V must be zeros for those that do not, so it enters
@@ -63,6 +67,7 @@ constexpr int kTile = 128;           // rows of an MMA
 constexpr int kRows = 2 * kTile;     // rows of a unit
 constexpr int kKeys = 64;            // keys of a step
 constexpr int kFlags = 16;           // steps whose tiles' validity is remembered
+constexpr uint32_t kOdd = 16;        // some token of the step is one that s_odd names
 constexpr float kRescale = 8.0f;     // log2 units
 // A unit's start and end in steps: its queries, the pipeline's filling, the
 // epilogue (some 12 us against 1.5 us a step; 5 to 10 measured the same).
@@ -152,26 +157,44 @@ __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(NREG));
 }
 
-__device__ __forceinline__ uint32_t twice(__half x) {
-  const uint32_t u = __half_as_ushort(x);
-  return u | u << 16;
-}
+constexpr uint32_t kHalves = 0x38003800u;  // 1/2, 1/2
 
-// Eight codes (fp16 pairs) times their scale as 16 bytes, or, SPLIT, times the
-// scale's upper eight bits and, `rest` bytes on, times what is left of it.
+// Eight codes (fp16 pairs) times their scale (in both halves of a word) as 16
+// bytes, or, SPLIT, times the scale's upper eight bits and, `rest` bytes on, times
+// what is left of it.
 template <bool SPLIT>
-__device__ __forceinline__ void put_chunk(uint8_t* to, int rest, __half scale, uint32_t a, uint32_t b,
-                                          uint32_t c, uint32_t d) {
+__device__ __forceinline__ void put_chunk(uint8_t* to, int rest, uint32_t scale, uint32_t a,
+                                          uint32_t b, uint32_t c, uint32_t d) {
   if constexpr (SPLIT) {
-    const __half upper = __ushort_as_half(__half_as_ushort(scale) & 0xFFF8u);
-    const uint32_t u = twice(upper), r = twice(__hsub(scale, upper));
+    const uint32_t u = scale & 0xFFF8FFF8u, r = minus(scale, u);
     *reinterpret_cast<uint4*>(to) = make_uint4(times(a, u), times(b, u), times(c, u), times(d, u));
     *reinterpret_cast<uint4*>(to + rest) =
         make_uint4(times(a, r), times(b, r), times(c, r), times(d, r));
   } else {
-    const uint32_t u = twice(scale);
-    *reinterpret_cast<uint4*>(to) = make_uint4(times(a, u), times(b, u), times(c, u), times(d, u));
+    *reinterpret_cast<uint4*>(to) =
+        make_uint4(times(a, scale), times(b, scale), times(c, scale), times(d, scale));
   }
+}
+
+// The NG scales of one token's K or V, two to a word.
+template <int NG>
+__device__ __forceinline__ void scale_words(const uint8_t* at, uint32_t (&x)[(NG + 1) / 2]) {
+  if constexpr (NG == 4) {
+    const uint2 w = *reinterpret_cast<const uint2*>(at);
+    x[0] = w.x, x[1] = w.y;
+  } else if constexpr (NG == 2) {
+    x[0] = *reinterpret_cast<const uint32_t*>(at);
+  } else {
+    x[0] = *reinterpret_cast<const uint16_t*>(at);
+  }
+}
+// Whether one is 8192 (0x7000) or more, or a NaN.
+template <int N>
+__device__ __forceinline__ bool any_large(const uint32_t (&x)[N]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) top |= x[i] + 0x10001000u;
+  return top & 0x80008000u;
 }
 
 // A 16-byte chunk of row `row` (128-byte rows, 128-byte swizzle).
@@ -188,8 +211,9 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
   __shared__ int64_t s_found[2];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_last;
-  __shared__ uint32_t s_valid[kFlags];    // bit u: tile u of the step was copied
-  __shared__ uint32_t s_nan[kFlags][2];   // keys whose V has a NaN scale
+  __shared__ uint32_t s_valid[kFlags];    // bit u: tile u of the step was copied; kOdd: see s_odd
+  // keys of the step whose V has a NaN scale, whose K has a large one, whose V has one
+  __shared__ uint32_t s_odd[kFlags][3][2];
   begin_after();
   if (smem_u32(smem) & 1023u) {  // the swizzle counts from 1024-byte boundaries
     if (threadIdx.x == 0) atomicCAS(A.status, 0, int32_t(SPARGE_EUNSUPPORTED));
@@ -304,7 +328,8 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
           uint8_t* dst = smem + C::CODE + stage * C::RAW;
           if (lane == 0) {
             s_valid[n % kFlags] = there;
-            s_nan[n % kFlags][0] = s_nan[n % kFlags][1] = 0;
+#pragma unroll
+            for (int i = 0; i < 6; ++i) s_odd[n % kFlags][i / 2][i % 2] = 0;
             if (there)
               mbar_expect_tx(&bars.raw_full[stage], __popc(there) * C::CODES);
             else
@@ -431,38 +456,48 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
                             (n < 2 || mbar_wait(&bars.k_empty[b], ((n >> 1) - 1) & 1, abort, A.status)));
         if (!ok) break;
         const uint8_t* raw = smem + C::CODE + stage * C::RAW;
-        const uint32_t there = s_valid[n % kFlags];
+        const uint32_t there = s_valid[n % kFlags] & 15u;
         const int left = p.req.keys - (p.step0 + t) * kKeys;  // tokens of the step that exist
-        // a token of V with a NaN scale is told to the softmax warps
-        if (th < kKeys && th < left && (there >> (th >> 4) & 1u)) {
-          const __half* sv = reinterpret_cast<const __half*>(raw + (th >> 4) * C::CODES + 16 * D +
-                                                             (th & 15) * NG * 4) + NG;
-          bool nan = false;
-#pragma unroll
-          for (int i = 0; i < NG; ++i) nan |= __hisnan(sv[i]);
-          if (nan) atomicOr(&s_nan[n % kFlags][th >> 5], 1u << (th & 31));
-        }
+        // the scales by which threads 0-63 look at V's tokens, the others at K's (below)
+        uint32_t look[(NG + 1) / 2];
+        scale_words<NG>(raw + (th % kKeys >> 4) * C::CODES + 16 * D + (th & 15) * NG * 4 +
+                            (th < kKeys ? 2 * NG : 0), look);
         // K: word w = t (D / 32) + j of a token's row is its chunk 4 j + t; a thread
         // has the same word of every TOKS-th token
         {
           constexpr int WORDS = D / 8, TOKS = 128 / WORDS;  // 8 (d = 128) or 16 at once
           const int w = th % WORDS, j = w % (D / 32), chunk = 4 * j + w / (D / 32), t0 = th / WORDS;
           uint8_t* to = smem + C::K + b * C::KV + (chunk >> 3) * (kKeys * 128);
-          uint32_t word[kKeys / TOKS];
-          __half scale[kKeys / TOKS];
+          uint32_t word[kKeys / TOKS], scale[kKeys / TOKS];
+          const int group = j / (D / 32 / NG);
+          const uint32_t own = group & 1 ? 0x3232u : 0x1010u;
 #pragma unroll
           for (int k = 0; k < kKeys / TOKS; ++k) {
             const uint8_t* tile = raw + k * TOKS / 16 * C::CODES;
             const int tok = t0 + k * TOKS % 16;
             word[k] = *reinterpret_cast<const uint32_t*>(tile + tok * (D / 2) + w * 4);
-            scale[k] = reinterpret_cast<const __half*>(tile + 16 * D + tok * NG * 4)[j / (D / 32 / NG)];
+            uint32_t x[(NG + 1) / 2];
+            scale_words<NG>(tile + 16 * D + tok * NG * 4, x);
+            scale[k] = __byte_perm(NG == 4 && group & 2 ? x[(NG - 1) / 2] : x[0], 0u, own);
+            if (any_large(x)) scale[k] = times(scale[k], kHalves);
           }
 #pragma unroll
           for (int k = 0; k < kKeys / TOKS; ++k) {
             const uint32_t hi = word[k] >> 8;
-            put_chunk<SPLIT>(to + swizzled(t0 + k * TOKS, chunk & 7), C::ONE,
-                             __hmul(scale[k], __float2half(0.5f)), codes0(word[k], masks),
-                             codes4(word[k], masks), codes0(hi, masks), codes4(hi, masks));
+            put_chunk<SPLIT>(to + swizzled(t0 + k * TOKS, chunk & 7), C::ONE, scale[k],
+                             codes0(word[k], masks), codes4(word[k], masks), codes0(hi, masks),
+                             codes4(hi, masks));
+          }
+        }
+        // what the softmax warps have to know of a token
+        {
+          const int tok = th % kKeys;
+          if (any_large(look) && tok < left && (there >> (tok >> 4) & 1u)) {
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < NG; ++i) nan |= (look[i / 2] >> (16 * (i % 2)) & 0x7FFFu) > 0x7C00u;
+            atomicOr(&s_odd[n % kFlags][th >= kKeys ? 1 : (nan ? 0 : 2)][tok >> 5], 1u << (tok & 31));
+            atomicOr(&s_valid[n % kFlags], kOdd);
           }
         }
         fence_async_shared();
@@ -477,12 +512,12 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
         {
           const int tok = th % kKeys, h = th / kKeys;
           const uint8_t* tile = raw + (tok >> 4) * C::CODES;
-          const __half* scales =
-              reinterpret_cast<const __half*>(tile + 16 * D + (tok & 15) * NG * 4) + NG;
+          uint32_t x[(NG + 1) / 2];
+          scale_words<NG>(tile + 16 * D + (tok & 15) * NG * 4 + 2 * NG, x);
+          const bool large = any_large(x);
           const uint8_t* codes = tile + 8 * D + (4 * h * 16 + Kv4Tile::v_pos(tok & 15)) * 4;
           const bool in = (there >> (tok >> 4) & 1u) && tok < left;
-          uint32_t words[C::SLABS][4];
-          __half scale[NG];
+          uint32_t words[C::SLABS][4], scale[NG];
 #pragma unroll
           for (int w = 0; w < C::SLABS; ++w)
 #pragma unroll
@@ -490,8 +525,9 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
               words[w][k] = *reinterpret_cast<const uint32_t*>(codes + w * 512 + k * 64);
 #pragma unroll
           for (int i = 0; i < NG; ++i) {
-            scale[i] = __hmul(scales[i], __float2half(0.5f));
-            if (!in || __hisnan(scale[i])) scale[i] = __ushort_as_half(0);  // no row may meet it
+            scale[i] = __byte_perm(x[i / 2], 0u, i % 2 ? 0x3232u : 0x1010u);
+            if (large) scale[i] = times(scale[i], kHalves);
+            if (!in || (scale[i] & 0x7FFFu) > 0x7C00u) scale[i] = 0;  // no row may meet it
           }
 #pragma unroll
           for (int w = 0; w < C::SLABS; ++w) {
@@ -564,7 +600,7 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
         const int k = field < 255 ? 139 - field : 0, half_k = k >> 1;
         const auto two_to = [](int n) { return __uint_as_float(uint32_t(n + 127) << 23); };
         const float k1 = two_to(half_k), k2 = two_to(k - half_k);
-        f = 2.0f * A.scale_log2 * two_to(-half_k) * two_to(half_k - k);
+        f = A.scale_log2 * two_to(-half_k) * two_to(half_k - k);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
           const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -605,14 +641,18 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
           tmem_wait_ld_fence(r1);
         }
         const int seen = lim - (p.step0 + t) * kKeys;  // keys c < seen
-        const uint32_t there = s_valid[(g + t) % kFlags];
-        // whether some row of the warp does not see some key of the step
-        const uint32_t nan0 = s_nan[(g + t) % kFlags][0], nan1 = s_nan[(g + t) % kFlags][1];
-        if (nan0 | nan1) {
+        const uint32_t flags = s_valid[(g + t) % kFlags], there = flags & 15u;
+        const uint32_t(&odd)[3][2] = s_odd[(g + t) % kFlags];
+        if (flags & kOdd) {
+          const uint32_t nan[2] = {odd[0][0], odd[0][1]}, large[2] = {odd[1][0], odd[1][1]};
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if ((c < 32 ? nan0 : nan1) >> (c & 31) & 1u) raw[c] = 0x7FFFFFFFu;
+          for (int c = 0; c < 64; ++c) {
+            if (large[c >> 5] >> (c & 31) & 1u)
+              raw[c] = __float_as_uint(2.0f * __uint_as_float(raw[c]));
+            if (nan[c >> 5] >> (c & 31) & 1u) raw[c] = 0x7FFFFFFFu;
+          }
         }
+        // whether some row of the warp does not see some key of the step
         const bool masked = __any_sync(0xffffffffu, seen < kKeys || there != 15u);
         uint32_t vis[2] = {~0u, ~0u};  // bit c: key c is seen
         if (masked) {
@@ -683,6 +723,14 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
         float s0, s1;
         unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
         l += s0 + s1;
+        if (flags & kOdd) {
+          const uint32_t large[2] = {odd[2][0], odd[2][1]};
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {  // 1 or 2 in each half
+            const uint32_t two = large[c >> 5] >> (c & 31) & 3u;
+            pk[c / 2] = times(pk[c / 2], (two & 1u ? 0x4000u : 0x3C00u) | (two & 2u ? 0x40000000u : 0x3C000000u));
+          }
+        }
         tmem_st32(at_s, pk);
         tmem_wait_st();
         tc_fence_before();
@@ -701,7 +749,7 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
       const int64_t slot = 2 * int64_t(blockIdx.x) + (p.step0 > 0 ? 0 : 1);
       const int64_t part_row = slot * kRows + tile * kTile + r;
       const float top = m == -INFINITY ? kLow : m;
-      const float inv = l == 0.f ? 0.f : 2.0f / l;
+      const float inv = l == 0.f ? 0.f : 1.0f / l;
       if (active && ok) {
         const int64_t orow = row_ok ? out_row(A, p.req, p.kvh, row) : 0;
 #pragma unroll 1
@@ -784,7 +832,7 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
           const int64_t orow = out_row(A, p.req, p.kvh, p.row0 + rr);
 #pragma unroll
           for (int v = 0; v < V; v += 2)
-            write_out(A, orow, D, V * lane + v, big, sum, 2.0f * x[v], 2.0f * x[v + 1]);
+            write_out(A, orow, D, V * lane + v, big, sum, x[v], x[v + 1]);
         }
       }
       __syncthreads();

@@ -364,7 +364,8 @@ size_t sparge_kv4_workspace_bytes(const sparge_kv4_t* c, const sparge_kv4_attn_t
  * (where this scale is at least 2^-12; 2^-39 itself below).
  * Requests with more than 64 rows for a KV head (new tokens times Hq / Hkv; of a call's only
  * request, max_q tokens) go through tiles of K and V in fp16: there the values c * s are taken
- * as they are for fp16 rows and rounded to fp16 (by up to 2^-11 of each) for bf16 rows, and a
+ * as they are for fp16 rows and rounded to fp16 (by up to 2^-11 of each) for bf16 rows (a token of
+ * K or of V with a scale of 8192 or more: its other scales to multiples of 2^-23), and a
  * NaN scale of V makes every channel NaN in the rows that see its token, not its group's alone.
  * Keys at pages outside [0, num_pages) or behind max_len are left out; these, a length below
  * 0 and a cu_q that does not ascend within [0, T] by steps of at most max_q (such a request
