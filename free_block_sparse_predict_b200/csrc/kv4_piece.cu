@@ -36,7 +36,7 @@
 // scores, or its weight in P, doubled: bits beside those of NaN scales tell the
 // softmax warps.  (All rows halved lost the last bit of scales below 2^-13, and 2^-24
 // itself.)  Q is fp16
-// with one power of two per row, P is fp16 of weights up to 2^8, sums are
+// with one power of two per row, P is fp16 of weights up to 2^8, times 2^6, sums are
 // float32.  A token whose scale of V is NaN makes the rows that see it NaN in
 // every channel: its row of V must be zeros for those that do not, so it enters
 // by its scores.
@@ -69,6 +69,10 @@ constexpr int kKeys = 64;            // keys of a step
 constexpr int kFlags = 16;           // steps whose tiles' validity is remembered
 constexpr uint32_t kOdd = 16;        // some token of the step is one that s_odd names
 constexpr float kRescale = 8.0f;     // log2 units
+// Weights are held times 2^kLift, so that P, which may be doubled, ends at 2^15 and
+// keeps its bits down to 2^-20 of the row's largest instead of 2^-14.
+constexpr float kLift = 6.0f;
+static_assert(kRescale + kLift + 1 <= 15, "P in fp16");
 // A unit's start and end in steps: its queries, the pipeline's filling, the
 // epilogue (some 12 us against 1.5 us a step; 5 to 10 measured the same).
 constexpr int kUnitSteps = 8;
@@ -698,7 +702,7 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
           if (rescale) l *= shrink;
         }
         if (grow) m = high;
-        const float nb = m == -INFINITY ? 0.f : -m;
+        const float nb = m == -INFINITY ? 0.f : kLift - m;
         const uint64_t f2 = pack2(f, f), nb2 = pack2(nb, nb);
         uint32_t pk[32];
         uint64_t sum[4] = {0, 0, 0, 0};
@@ -790,7 +794,7 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
           if (p.cut)
             A.part_ml[part_row] = make_float2(top, l);
           else if (A.lse != nullptr)
-            A.lse[orow] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+            A.lse[orow] = l == 0.f ? -INFINITY : (top + (log2f(l) - kLift)) * 0.6931471805599453f;
         }
       }
       tc_fence_before();
@@ -832,7 +836,7 @@ __global__ void __launch_bounds__(kPieceThreads, 1) kv4_piece_kernel(const __gri
           const int64_t orow = out_row(A, p.req, p.kvh, p.row0 + rr);
 #pragma unroll
           for (int v = 0; v < V; v += 2)
-            write_out(A, orow, D, V * lane + v, big, sum, x[v], x[v + 1]);
+            write_out(A, orow, D, V * lane + v, big - kLift, sum, x[v], x[v + 1]);
         }
       }
       __syncthreads();

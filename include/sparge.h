@@ -361,7 +361,8 @@ size_t sparge_kv4_workspace_bytes(const sparge_kv4_t* c, const sparge_kv4_attn_t
  * statistics are float32; a weight, and its product with V's scale, are rounded to fp16, held
  * times powers of two so that they keep all their bits down to a weight of 2^-24 of the row's
  * largest and, for a product, 2^-27 of what that weight and the KV head's largest scale would give
- * (where this scale is at least 2^-12; 2^-39 itself below).
+ * (where this scale is at least 2^-12; 2^-39 itself below), in the tiles of the next paragraph
+ * down to a weight of 2^-20.
  * Requests with more than 64 rows for a KV head (new tokens times Hq / Hkv; of a call's only
  * request, max_q tokens) go through tiles of K and V in fp16: there the values c * s are taken
  * as they are for fp16 rows and rounded to fp16 (by up to 2^-11 of each) for bf16 rows (a token of

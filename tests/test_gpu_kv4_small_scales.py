@@ -23,8 +23,8 @@ TINY = 2.0 ** -24
 LEAST = 2.0 ** -14      # weights from here on keep 11 bits
 
 
-def check_pieces(case, scale=None):
-    """One request per case; see above."""
+def check_pieces(case, scale=None, least=LEAST):
+    """One request per case; see above.  least: the smallest weight with 11 bits."""
     got = case.run(scale=scale)
     torch.cuda.synchronize()
     assert fb.sparge_device_status(case.ws) == 0
@@ -38,7 +38,7 @@ def check_pieces(case, scale=None):
     see = torch.arange(n, device=dev())[None] <= (n - m + torch.arange(m, device=dev()))[:, None]
     s = s.masked_fill(~see[:, None], -np.inf)
     p = torch.exp(s - s.amax(-1, keepdim=True))
-    light = torch.where(p < LEAST, p.clamp(max=LEAST * 2.0 ** -11), torch.zeros_like(p))
+    light = torch.where(p < least, p.clamp(max=least * 2.0 ** -11), torch.zeros_like(p))
     loose = torch.einsum("ihn,nhd->ihd", light, v.abs())
     tol = (2.0 ** -11 * (2 if bf16 else 1) + 2 * w + 8 * (keys / 64 + 2) * 2.0 ** -22)[..., None] * size
     tol = tol * (1 + 2.0 ** -8) + loose
