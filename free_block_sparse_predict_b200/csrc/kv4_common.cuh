@@ -15,7 +15,9 @@ namespace sparge {
 namespace kv4 {
 
 constexpr int kSms = 148;
-constexpr float kLow = -1e30f;     // "no key yet"; finite, so differences stay numbers
+// "No key yet": finite, so that differences stay numbers, and below every finite score
+// (scales reach 2^100).
+constexpr float kLow = -3.402823466e38f;
 
 struct Masks {
   uint32_t low, high, mixed;  // 0x000F000F, 0x00F000F0, 0x00F0000F
