@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
   // for the request is paid once for them; the first token of a new page writes
   // its table entry
   const int32_t end = s_cu[A.R];
+  static_assert(kMaxPlanTokens - 1 <= INT32_MAX - RUN, "t0 + RUN below fits 32 bits");
   const int64_t runs = (int64_t(A.max_tokens) + RUN - 1) / RUN;
   const bool vec = (reinterpret_cast<uintptr_t>(A.slot_map) & 15u) == 0;
   for (int64_t n = int64_t(rank) * kPlanThreads + threadIdx.x; n < runs;

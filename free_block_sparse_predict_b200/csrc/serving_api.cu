@@ -177,7 +177,7 @@ sparge_status_t sparge_kv_plan(int32_t R, int32_t page_size, int32_t max_pages,
   if (R < 0 || page_size < 1 || max_pages < 0 || num_pages < 0 || max_tokens < 0)
     return SPARGE_EINVAL;
   if (R > kMaxPlanRequests || int64_t(num_pages) * page_size > INT32_MAX ||
-      int64_t(max_pages) * page_size > INT32_MAX)
+      int64_t(max_pages) * page_size > INT32_MAX || max_tokens > kMaxPlanTokens)
     return SPARGE_EUNSUPPORTED;
   // what has no elements may be NULL
   if (free_count == nullptr || free_count_out == nullptr || cu_new == nullptr) return SPARGE_EINVAL;

@@ -147,6 +147,7 @@ cudaError_t launch_rope(const sparge_rope_t& p, const void* src, const int64_t* 
 
 // ------------------------------------------------------------- kv_plan.cu
 constexpr int kMaxPlanRequests = 4096;
+constexpr int32_t kMaxPlanTokens = INT32_MAX - 15;  // a run behind the last token fits 32 bits
 struct KvPlanArgs {  // as sparge_kv_plan's arguments
   int32_t R, page_size, max_pages, num_pages, max_tokens;
   const int32_t* new_len;

@@ -276,7 +276,8 @@ sparge_status_t sparge_rope_inverse(const sparge_rope_t* p, const void* y, void*
  * [0, max_pages * page_size] are taken as the nearer end, a height outside [0, num_pages]
  * likewise; what would be pushed past num_pages is dropped.
  * The outputs may not overlap one another or the inputs, apart from the two named above.
- * SPARGE_EUNSUPPORTED: R > 4096, or num_pages or max_pages times page_size >= 2^31. */
+ * SPARGE_EUNSUPPORTED: R > 4096, num_pages or max_pages times page_size >= 2^31, or
+ * max_tokens > 2^31 - 16. */
 sparge_status_t sparge_kv_plan(int32_t R, int32_t page_size, int32_t max_pages,
                                int32_t num_pages, int32_t max_tokens, const int32_t* new_len,
                                const int32_t* seq_len, int32_t* block_table,
