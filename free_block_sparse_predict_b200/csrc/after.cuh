@@ -30,9 +30,7 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  if (e != cudaSuccess) cudaGetLastError();  // ours to report, not the next caller's
-  return e;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace sparge

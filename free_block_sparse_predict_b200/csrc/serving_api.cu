@@ -11,8 +11,10 @@ namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// (the failed call's error is reported here, not by the next call that asks for the last)
 sparge_status_t from_cuda(cudaError_t e) {
   if (e == cudaSuccess) return SPARGE_OK;
+  cudaGetLastError();
   if (e == cudaErrorNotSupported) return SPARGE_EUNSUPPORTED;
   return SPARGE_ECUDA;
 }
