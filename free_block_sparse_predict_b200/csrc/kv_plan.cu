@@ -312,9 +312,13 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, cudaStream_t stream) {
   // to 4096 tokens, 29 us in a cluster of sixteen.  The grid's barrier costs
   // about 2 us more than a cluster's: 16,000 tokens take 7.3 us in a cluster and
   // 9.3 us in the grid, 64,000 tokens 13.6 and 8.7 us.
-  constexpr int kSms = 148, kCluster = 8;
-  return a.max_tokens <= 4 * kCluster * kPlanThreads ? run<1, false>(a, kCluster, stream)
-                                                     : run<4, true>(a, kSms, stream);
+  constexpr int kCluster = 8;
+  if (a.max_tokens <= 4 * kCluster * kPlanThreads) return run<1, false>(a, kCluster, stream);
+  // a cooperative grid has to be resident at once: a CTA per SM of this device
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? run<4, true>(a, sms, stream) : e;
 }
 
 }  // namespace sparge
