@@ -75,7 +75,8 @@ __device__ __forceinline__ int32_t pages_of(int32_t tokens, const Div& page) {
 // RUN: consecutive tokens per thread and step.  GRID: the CTAs are the whole
 // cooperative grid instead of one cluster.
 template <int RUN, bool GRID>
-__global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs A, const Div page) {
+__global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs A, const Div page,
+                                                               const uint32_t id_end) {
   namespace cg = cooperative_groups;
   const int rank = int(blockIdx.x), ctas = int(gridDim.x);
   __shared__ int64_t sh1[64], sh2[32];
@@ -221,18 +222,22 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
         if (write) *entry = id;
         return id;
       };
-      const auto first_slot = [&](int32_t id) { return int32_t(uint32_t(id) * uint32_t(P)); };
+      // (a number whose slots pass 32 bits is no page's: slots below 0, not another page's)
+      const auto first_slot = [&](int32_t id) {
+        const bool fits = uint32_t(id) < id_end || uint32_t(~id) < id_end;
+        return fits ? uint32_t(id) * uint32_t(P) : 0x80000000u;
+      };
       if (RUN > 1 && t0 + RUN <= s_cu[r + 1] && P >= RUN) {
         // all of one request and of one or two of its pages: nearly every run
         const int32_t len = s_len[r];
         if (len >= 0) {
           const int32_t pos = len + (t0 - s_cu[r]), p = page.quot(pos), have = pages_of(len, page);
           const int32_t in = pos - p * P;
-          const int32_t a = first_slot(page_id(r, p, have, in == 0)) + in;
-          int32_t b = 0;  // so that b + i is token i's slot, if it is in the next page
+          const uint32_t a = first_slot(page_id(r, p, have, in == 0)) + in;
+          uint32_t b = 0;  // so that b + i is token i's slot, if it is in the next page
           if (in + RUN > P) b = first_slot(page_id(r, p + 1, have, true)) + in - P;
 #pragma unroll
-          for (int i = 0; i < RUN; ++i) slot[i] = (in + i < P ? a : b) + i;
+          for (int i = 0; i < RUN; ++i) slot[i] = int32_t((in + i < P ? a : b) + i);
         }
       } else {
         int32_t next = s_cu[r + 1];    // where the request's tokens end
@@ -245,7 +250,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const KvPlanArgs 
           if (in == P) {  // another page
             const int32_t pos = len + (t - s_cu[r]), p = page.quot(pos);
             in = pos - p * P;
-            slot_at = first_slot(page_id(r, p, pages_of(len, page), in == 0)) + in;
+            slot_at = int32_t(first_slot(page_id(r, p, pages_of(len, page), in == 0)) + in);
           }
 #pragma unroll
           for (int k = 0; k < RUN; ++k)
@@ -299,7 +304,8 @@ cudaError_t run(const KvPlanArgs& a, int max_ctas, cudaStream_t stream) {
   }
   cfg.attrs = attr;
   cfg.numAttrs = GRID ? 1 : 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a, make_div(uint32_t(a.page_size)));
+  return cudaLaunchKernelEx(&cfg, kernel, a, make_div(uint32_t(a.page_size)),
+                            0x80000000u / uint32_t(a.page_size));
 }
 
 }  // namespace

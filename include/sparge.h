@@ -274,7 +274,8 @@ sparge_status_t sparge_rope_inverse(const sparge_rope_t* p, const void* y, void*
  *   admitted     int32 [R]: 0 for a request whose new tokens found no room, else 1
  * A request that is not admitted keeps its length and its pages.  Lengths outside
  * [0, max_pages * page_size] are taken as the nearer end, a height outside [0, num_pages]
- * likewise; what would be pushed past num_pages is dropped.
+ * likewise; what would be pushed past num_pages is dropped.  Page numbers are taken as they are; one whose
+ * slots do not fit 32 bits gives slots below 0.
  * The outputs may not overlap one another or the inputs, apart from the two named above.
  * SPARGE_EUNSUPPORTED: R > 4096, num_pages or max_pages times page_size >= 2^31, or
  * max_tokens > 2^31 - 16. */
