@@ -95,7 +95,7 @@ sparge_status_t check_attn(const sparge_kv4_t* c, const sparge_kv4_attn_t* a) {
       !(a->scale > 0.f) || !(a->scale <= 0x1p100f) ||
       (a->dtype != SPARGE_F16 && a->dtype != SPARGE_BF16))
     return SPARGE_EINVAL;
-  if (a->T > 1 && (a->q_stride < int64_t(a->Hq) * c->d || a->q_stride > (int64_t(1) << 40)))
+  if (a->T > 1 && (a->q_stride < int64_t(a->Hq) * c->d || a->q_stride > (int64_t(1) << 58) / a->T))
     return SPARGE_EINVAL;
   if (a->T > 1 && a->q_stride % 8 != 0) return SPARGE_EUNSUPPORTED;
   if (a->R > 65535 || int64_t(a->T) * a->Hq > INT32_MAX ||
