@@ -251,37 +251,49 @@ def predict_outputs(params: SpargeParams, device="cuda"):
             torch.empty((B, Hkv, Tn), dtype=torch.float32, device=device))
 
 
+def _torch_stream(stream, device):
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    address = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return torch.cuda.ExternalStream(address, device) if address else torch.cuda.default_stream(device)
+
+
 def sparge_forward(params, q, k, v, perm=None, ws=None, stats=None, stream=None, rope=None):
     """rotary positions and permute (optional) -> predict -> attention -> inverse permute.
 
     Returns (o, mask, kv_idx, kv_cnt).  ``perm`` is a device table from
     sparge_hilbert_index; ``ws`` a workspace of sparge_workspace_bytes; ``rope`` a
     Rope whose angles turn q and k first, in the same pass that permutes them (q and
-    k may then have any strides)."""
+    k may then have any strides).  With ``stream`` all of it is allocated and runs there."""
+    if stream is not None:
+        # memory that goes back to the current stream's pool would be handed on there
+        # before the kernels of the other have read it, and a fresh workspace's zeros
+        # would not come before them
+        with torch.cuda.stream(_torch_stream(stream, q.device)):
+            return sparge_forward(params, q, k, v, perm, ws, stats, None, rope)
     dev = q.device
     if ws is None:
         ws = workspace(params, dev)
     if rope is not None:
         qp, kp = (torch.empty(x.shape, dtype=x.dtype, device=dev) for x in (q, k))
         for x, y in ((q, qp), (k, kp)):
-            sparge_rope_apply(x, y, rope.pos, rope.inv_freq, rope.axis, perm, rope.interleaved,
-                              stream)
+            sparge_rope_apply(x, y, rope.pos, rope.inv_freq, rope.axis, perm, rope.interleaved)
         q, k = qp, kp
     if perm is not None:
         if rope is None:
             qp, kp = torch.empty_like(q), torch.empty_like(k)
-            sparge_hilbert_permute(q, qp, perm, stream)
-            sparge_hilbert_permute(k, kp, perm, stream)
+            sparge_hilbert_permute(q, qp, perm)
+            sparge_hilbert_permute(k, kp, perm)
         vp = torch.empty_like(v)
-        sparge_hilbert_permute(v, vp, perm, stream)
+        sparge_hilbert_permute(v, vp, perm)
         q, k, v = qp, kp, vp
     mask, kv_idx, kv_cnt, s_q, s_k = predict_outputs(params, dev)
-    sparge_predict_mask(params, q, k, mask, kv_idx, kv_cnt, None, None, ws, stream)
+    sparge_predict_mask(params, q, k, mask, kv_idx, kv_cnt, None, None, ws)
     odt = {SPARGE_F16: torch.float16, SPARGE_BF16: torch.bfloat16, SPARGE_F32: torch.float32}
     o = torch.empty(q.shape, dtype=odt[params.o_dtype], device=dev)
-    sparge_attn_fwd(params, q, k, v, kv_idx, kv_cnt, o, ws, stats, stream)
+    sparge_attn_fwd(params, q, k, v, kv_idx, kv_cnt, o, ws, stats)
     if perm is not None:
         out = torch.empty_like(o)
-        sparge_inverse_permute(o, out, perm, stream)
+        sparge_inverse_permute(o, out, perm)
         o = out
     return o, mask, kv_idx, kv_cnt
