@@ -81,13 +81,13 @@ def build(extra=(), verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
         binding = ex.submit(_binding)
         objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-        binding.result()
     newest = max(os.path.getmtime(o) for o in objs)
     if not os.path.exists(LIB) or os.path.getmtime(LIB) < newest:
         cmd = [nvcc(), "-shared", "-o", LIB] + objs + ARCH
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    binding.result()  # behind the C library, which knows nothing of torch
     if verbose:
         print(LIB)
     return LIB
