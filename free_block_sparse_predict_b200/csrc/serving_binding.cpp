@@ -382,4 +382,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_serving", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__serving() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__serving() {
+  PyObject* m = PyModule_Create(&module);
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", SPARGE_TORCH_VERSION) != 0)
+    Py_CLEAR(m);
+  return m;
+}

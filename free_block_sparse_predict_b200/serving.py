@@ -40,8 +40,13 @@ def _load():
     try:
         module = importlib.import_module("._serving", __package__)
     except ImportError as e:
-        raise ImportError(f"_serving.so cannot be loaded ({e}); build it with "
+        raise ImportError(f"_serving cannot be loaded ({e}); build it with "
                           "`python -m free_block_sparse_predict_b200.build`") from e
+    if module.torch_version != str(torch.__version__):
+        # it reads torch's objects by their layout
+        raise ImportError(f"_serving was built for torch {module.torch_version}, this is "
+                          f"{torch.__version__}; build it again with "
+                          "`python -m free_block_sparse_predict_b200.build`")
     module.setup(SpargeError, torch._C._cuda_getCurrentRawStream, _entries)
     _serving = module
     return module
