@@ -8,10 +8,10 @@
 
 namespace sparge {
 
-// First of all in a kernel launched by launch_after: lets the next kernel's CTAs
-// come to the SMs that have room, and waits until all that earlier kernels
-// wrote is there.  Nothing is read or written before it, and every CTA passes it, so a
-// kernel that ends has seen all before it end.
+// Before a kernel launched by launch_after touches global or tensor memory (its own
+// shared memory it may): lets the next kernel's CTAs come to the SMs that have
+// room, and waits until all that earlier kernels wrote is there.  Every CTA passes it,
+// so a kernel that ends has seen all before it end.
 __device__ __forceinline__ void begin_after() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");

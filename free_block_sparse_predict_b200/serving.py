@@ -110,7 +110,8 @@ def sparge_rope_apply(x, y, pos, inv_freq, axis, perm: Optional[torch.Tensor] = 
 
 def sparge_rope_inverse(y, x, pos, inv_freq, axis, perm: Optional[torch.Tensor] = None,
                         interleaved: bool = False, stream=None) -> None:
-    """x[b, h, s] = y[b, h, p] turned back: the inverse of sparge_rope_apply and its gradient."""
+    """x[b, h, s] = y[b, h, p] turned back: the inverse of sparge_rope_apply, and its gradient
+    where perm names no row twice."""
     (_serving or _load()).rope(x, y, pos, inv_freq, axis, perm, interleaved, True, stream)
 
 

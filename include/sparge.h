@@ -233,7 +233,8 @@ typedef struct {
  *   pos       device int32 [B or 1, axes, N]
  *   inv_freq  device float64 [rot/2], radians per position (any frequency scaling is in it)
  *   axis      device int32 [rot/2], which axis turns pair i, in [0, axes) (others: a = 0)
- *   perm      device int32 [N] or NULL; rows whose entry lies outside [0, N) are skipped
+ *   perm      device int32 [N] or NULL; rows whose entry lies outside [0, N) are skipped.  An
+ *             entry may come twice here, but not in the inverse
  * The angle is reduced in float64 turns, so far positions lose nothing: for |inv_freq| <= 1 its
  * error is below 2^-23 of a turn up to position 2^30.  The products are float32, rounded once
  * to dtype.
@@ -248,7 +249,8 @@ sparge_status_t sparge_rope_apply(const sparge_rope_t* p, const void* x, void* y
 
 /* The inverse, which is also the gradient of sparge_rope_apply (the rotation is
  * orthogonal): x[b, h, s, :] = y[b, h, p, :] turned by -a.  Same rules; with perm, rows of x
- * that no entry names are left as they were. */
+ * that no entry names are left as they were, and of rows that two entries name each 16 bytes are
+ * one of the two's and which is unspecified (not their sum, as a gradient would have it). */
 sparge_status_t sparge_rope_inverse(const sparge_rope_t* p, const void* y, void* x,
                                     const int32_t* pos, const double* inv_freq,
                                     const int32_t* axis, const int32_t* perm,
@@ -268,7 +270,9 @@ sparge_status_t sparge_rope_inverse(const sparge_rope_t* p, const void* y, void*
  * those of every earlier such request, are there; one that needs no new page is always
  * admitted then.  Pages are popped from the top, request by request.
  *   seq_len_out, free_count_out  the new values (may be seq_len and free_count themselves)
- *   cu_new       int32 [R + 1]: where each request's new tokens start (cu_q of the attention)
+ *   cu_new       int32 [R + 1]: where each request's new tokens start (cu_q of the attention),
+ *                those of requests that were not admitted counted too: their rows' attention
+ *                means nothing
  *   slot_map     int32 [max_tokens]: page * page_size + offset of new token t; -1 for a
  *                token of a request that was not admitted and behind the last token
  *   admitted     int32 [R]: 0 for a request whose new tokens found no room, else 1
@@ -373,6 +377,8 @@ size_t sparge_kv4_workspace_bytes(const sparge_kv4_t* c, const sparge_kv4_attn_t
  * Keys at pages outside [0, num_pages) or behind max_len are left out; these, a length below
  * 0 and a cu_q that does not ascend within [0, T] by steps of at most max_q (such a request
  * is skipped) put SPARGE_EINVAL into the workspace's status word (sparge_device_status).
+ * A call gives the same bits every time.  They depend on the whole call: the work is cut over all
+ * of its requests, and of a call's only request max_q alone says which tiles it goes through.
  * SPARGE_EUNSUPPORTED: R or Hkv > 65535, or more than 2^31 - 1 rows of q times heads. */
 sparge_status_t sparge_kv4_attn(const sparge_kv4_t* c, const sparge_kv4_attn_t* a,
                                 const void* q, const void* cache, const int32_t* block_table,
