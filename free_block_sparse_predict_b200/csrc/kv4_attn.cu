@@ -801,9 +801,14 @@ struct Plan {
 
 // More rows than this per request and KV head (tokens times the group's heads)
 // are a piece of a prompt, kv4_piece.cu, whose steps cost about the same for up
-// to 256 rows, while here every 16 rows read the codes again.  16 requests of up
-// to 32,768 keys, 8 KV heads of 128 channels, here and there: 338 and 405 us for
-// 48 rows, 445 and 457 for 64, 632 and 448 for 96, 1598 and 569 for 256.
+// to 256 rows, while here every 16 rows read the codes again.  16 requests of 11,000
+// to 32,768 keys, 8 KV heads, here and there in us:
+//              32 rows      48 rows      64 rows      96 rows
+//   128 bf16   225 / 388    328 / 392    432 / 371    637 / 382
+//   128 fp16   225 / 415    328 / 420    432 / 411    637 / 418
+//    64 bf16   161 / 350    235 / 354    309 / 344    456 / 351
+//    64 fp16   161 / 362    235 / 366    309 / 351    456 / 360
+// Two requests of up to 8192 keys are latency, and here is faster up to 128 rows (44 / 98).
 constexpr int64_t kFewRows = 64;
 
 // CTAs from the bounds that the host knows (lengths are on the device): all

