@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kAttnThreads, Cfg<D, NG, NT>::CTAS)
   constexpr int COST = kUnitKeys / KEYS;
   constexpr int BATCH_STEPS = 32 / TPS;  // steps whose tile numbers a warp fetches at once
   static_assert(ST < BATCH_STEPS, "steps in flight lie in two batches");
+  static_assert(KEYS == 32, "V's scales of a step: a lane a token");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t full[kWarps][ST];
   __shared__ float2 s_ml[kWarps][C::ROWS];
